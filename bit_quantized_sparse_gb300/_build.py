@@ -20,7 +20,7 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmoe_w4.so")
 LIB_DEBUG = os.path.join(PKG, "libmoe_w4_debug.so")
 SOURCES = ["api.cu", "router.cu", "grouping.cu", "decode.cu", "grouped_gemm.cu", "noalloc.cu", "decode_fused.cu",
-           "ablation.cu"]
+           "ablation.cu", "kv_cache.cu", "attend.cu", "logprobs.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
          "-I", os.path.join(ROOT, "include"), "-I", CSRC]
@@ -43,7 +43,7 @@ def build(verbose=False, force=False, debug=False):
     flags = FLAGS + (["-DMW4_DEBUG_CHECKS"] if debug else [])
     os.makedirs(bdir, exist_ok=True)
     headers = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".h", ".cuh"))]
-    headers.append(os.path.join(ROOT, "include", "moe_w4.h"))
+    headers += [os.path.join(ROOT, "include", h) for h in ("moe_w4.h", "moe_w4_serving.h")]
     objs, jobs = [], []
     for src in SOURCES:
         s = os.path.join(CSRC, src)

@@ -434,12 +434,14 @@ int moe_w4_ablation_prefill(const moe_w4_layer* L, int T, const moe_w4_bf16* x, 
 const char* moe_w4_strerror(int status) {
     switch (status) {
         case MOE_W4_OK: return "ok";
-        case MOE_W4_ERR_INVALID: return "invalid argument (NULL pointer, negative T or top_k out of range)";
-        case MOE_W4_ERR_UNSUPPORTED: return "unsupported shape (H and I multiples of 128, H, I <= 4096, E <= 1024, decode T <= 16)";
-        case MOE_W4_ERR_WORKSPACE: return "workspace missing, smaller than moe_w4_workspace_size or not 256-byte aligned";
+        case MOE_W4_ERR_INVALID: return "invalid argument (NULL pointer, a negative or inconsistent size, top_k out of range)";
+        case MOE_W4_ERR_UNSUPPORTED: 
+            return "unsupported shape or type (layer: H and I multiples of 128, H, I <= 4096, E <= 1024, decode T <= 16; "
+                   "cache: bf16 or fp16, head_dim 64, 128 or 256)";
+        case MOE_W4_ERR_WORKSPACE: return "workspace missing, smaller than the call's workspace size or not 256-byte aligned";
         case MOE_W4_ERR_LAUNCH: return "a CUDA kernel launch failed";
         case MOE_W4_ERR_DEVICE: return "a kernel reported a device-side error in the status word";
-        case MOE_W4_ERR_ALIGN: return "a pointer is not 16-byte aligned";
+        case MOE_W4_ERR_ALIGN: return "a pointer or stride is not aligned (16 bytes where not stated otherwise)";
         case MOE_W4_ERR_SCRATCH:
             return "the call needs more scratch than the fixed MOE_W4_NOALLOC_SCRATCH_BYTES array of "
                    "moe_w4_forward_decode_noalloc";

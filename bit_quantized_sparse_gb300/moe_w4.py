@@ -7,11 +7,13 @@ Importing this module raises ImportError if the library has not been built
 Two levels:
   * the C entry points under their own names (moe_w4_route,
     moe_w4_forward_decode, moe_w4_forward_prefill, moe_w4_workspace_size,
-    moe_w4_workspace_init, moe_w4_status_offset, moe_w4_strerror), taking raw
-    device pointers (ints), a MoeW4Layer struct and a stream handle;
+    moe_w4_workspace_init, moe_w4_status_offset, moe_w4_strerror; the cache,
+    attention and log-probability calls of include/moe_w4_serving.h), taking raw
+    device pointers (ints), a MoeW4Layer or MoeW4KvCache struct and a stream handle;
   * `DeviceLayer`, which keeps a layer's tensors on the GPU, and `route`,
     `forward_decode`, `forward_prefill`, which take torch tensors, allocate
-    outputs with torch and raise MoeW4Error on a non-zero status.
+    outputs with torch and raise MoeW4Error on a non-zero status (serving.py has
+    these for the operators around the layer).
 """
 from __future__ import annotations
 
@@ -32,6 +34,7 @@ if not os.path.exists(LIB_PATH):
 _lib = ctypes.CDLL(LIB_PATH)
 
 c_int, c_size_t, c_void_p, c_char_p = ctypes.c_int, ctypes.c_size_t, ctypes.c_void_p, ctypes.c_char_p
+c_int64, c_float = ctypes.c_int64, ctypes.c_float
 
 MOE_W4_OK = 0
 MOE_W4_ERR_INVALID = -1
@@ -53,6 +56,11 @@ DECODE_MAX_T = 16
 MAX_TOKENS = 1 << 22                 # MOE_W4_MAX_TOKENS
 MOE_W4_PATH_FUSED_ROWS = 1           # moe_w4_decode_path
 MOE_W4_PATH_GROUPED = 2
+# include/moe_w4_serving.h
+MOE_W4_TYPE_BF16 = 0
+MOE_W4_TYPE_FP16 = 1
+MOE_W4_TYPE_FP32 = 2
+CTRL_BYTES = 256                     # MOE_W4_CTRL_BYTES
 
 
 class MoeW4Mat(ctypes.Structure):
@@ -67,7 +75,20 @@ class MoeW4Layer(ctypes.Structure):
                 ("code_format", c_int), ("router_prep", c_void_p)]
 
 
+class MoeW4KvCache(ctypes.Structure):      # include/moe_w4_serving.h
+    _fields_ = [("dtype", c_int), ("n_kv_heads", c_int), ("head_dim", c_int), ("page_size", c_int),
+                ("num_pages", c_int), ("page_stride", c_int64), ("head_stride", c_int64), ("slot_stride", c_int64),
+                ("k", c_void_p), ("v", c_void_p), ("n_seqs", c_int), ("pages_per_seq", c_int),
+                ("table_stride", c_int64), ("block_table", c_void_p), ("seq_lens", c_void_p)]
+
+
+class MoeW4KvTrack(ctypes.Structure):
+    _fields_ = [("weight", c_void_p), ("pos", c_void_p), ("seq_stride", c_int64), ("head_stride", c_int64),
+                ("slots", c_int)]
+
+
 _P = ctypes.POINTER(MoeW4Layer)
+_KV, _TR = ctypes.POINTER(MoeW4KvCache), ctypes.POINTER(MoeW4KvTrack)
 _SIGS = {
     "moe_w4_workspace_size": (c_size_t, [_P, c_int]),
     "moe_w4_router_prep_bytes": (c_size_t, [_P]),
@@ -94,6 +115,16 @@ _SIGS = {
     "moe_w4_test_block_records_bytes": (c_size_t, [_P, c_int]),
     "moe_w4_test_block_records": (c_int, [_P, c_int, c_void_p, c_size_t, c_void_p, c_size_t, c_void_p]),
     "moe_w4_strerror": (c_char_p, [c_int]),
+    "moe_w4_kv_append": (c_int, [_KV, _TR, c_int, c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_void_p, c_void_p,
+                                 c_void_p, c_size_t, c_void_p]),
+    "moe_w4_attend_workspace_size": (c_size_t, [_KV, c_int, c_int, c_int]),
+    "moe_w4_attend_decode": (c_int, [_KV, c_int, c_void_p, c_int64, c_float, c_int, c_void_p, c_int64, c_void_p, _TR,
+                                     c_void_p, c_void_p, c_size_t, c_void_p]),
+    "moe_w4_evict_workspace_size": (c_size_t, [_KV, c_int, c_int]),
+    "moe_w4_kv_evict": (c_int, [_KV, _TR, c_void_p, c_int, c_int, c_int, c_int, c_void_p, c_void_p, c_void_p, c_void_p,
+                                c_size_t, c_void_p]),
+    "moe_w4_token_logprobs": (c_int, [c_int, c_int, c_int, c_void_p, c_int64, c_void_p, c_int, c_void_p, c_void_p,
+                                      c_void_p, c_void_p, c_void_p, c_size_t, c_void_p]),
 }
 for _name, (_res, _args) in _SIGS.items():
     _f = getattr(_lib, _name)
@@ -123,6 +154,12 @@ moe_w4_noalloc_test_skip_publish = _lib.moe_w4_noalloc_test_skip_publish
 moe_w4_test_skip_publish = _lib.moe_w4_test_skip_publish
 moe_w4_test_block_records_bytes = _lib.moe_w4_test_block_records_bytes
 moe_w4_test_block_records = _lib.moe_w4_test_block_records
+moe_w4_kv_append = _lib.moe_w4_kv_append
+moe_w4_attend_workspace_size = _lib.moe_w4_attend_workspace_size
+moe_w4_attend_decode = _lib.moe_w4_attend_decode
+moe_w4_evict_workspace_size = _lib.moe_w4_evict_workspace_size
+moe_w4_kv_evict = _lib.moe_w4_kv_evict
+moe_w4_token_logprobs = _lib.moe_w4_token_logprobs
 
 
 def moe_w4_strerror(status: int) -> str:
