@@ -18,8 +18,6 @@
 // Each warp is a pipeline of its own: it owns 16 tokens of every tile, keeps
 // them arriving through cp.async several tiles ahead (across row ends), and
 // holds its own running maximum, sum and output; warps meet only at row ends.
-#include <mutex>
-
 #include "serving.cuh"
 
 namespace mw4 {
@@ -31,7 +29,6 @@ constexpr int kTile = kSub * kAttWarps;
 constexpr int kHeads = 16;                      // query heads of a row, at most
 constexpr int kMaxCtas = 152 * 3;               // partial records the workspace has room for
 constexpr float kLazyRescale = 8.f;             // log2 growth of the maximum before a rescale
-constexpr float kLn2 = 0.693147180559945309f, kLog2e = 1.44269504088896341f;
 
 // Pipeline depth and CTAs per SM for a head size: about 100 to 200 KB of shared
 // memory of every SM holds tiles in flight.
@@ -96,11 +93,6 @@ MW4_DEV void ldsm4_t(uint32_t (&r)[4], uint32_t addr) {
 // 16 bytes, or zeros where !there (the source is not read then).
 MW4_DEV void cp_async_16_or_zero(uint32_t dst, const void* src, bool there) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" :: "r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
-}
-MW4_DEV float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
 }
 
 // The list of tiles and its shares.  total >= 1; part c of `parts` starts at
@@ -584,21 +576,10 @@ static AttendWs attend_ws(const moe_w4_kv_cache& c, int n_q_heads, int max_len, 
     return w;
 }
 
-static int sm_count() {
-    static std::mutex mu;
-    static int cached[64] = {};
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0) return 0;
-    std::lock_guard<std::mutex> lock(mu);
-    int v = dev < 64 ? cached[dev] : 0;
-    if (!v && cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
-    if (dev < 64) cached[dev] = v;
-    return v;
-}
-
 template <typename T, int D>
 static cudaError_t launch_attend(const AttendArgs& a, cudaStream_t st) {
-    const int sms = sm_count();
+    int dev = 0;
+    const int sms = sm_count(&dev);
     if (sms < 1) return cudaErrorInvalidDevice;
     constexpr int smem = AttCfg<D>::stages * kAttWarps * 2 * kSub * D * 2;
     const int64_t rows = (int64_t)a.c.n_seqs * a.c.n_kv_heads * a.head_blocks;
@@ -607,8 +588,9 @@ static cudaError_t launch_attend(const AttendArgs& a, cudaStream_t st) {
     int64_t ctas = (int64_t)sms * AttCfg<D>::ctas;
     if (ctas > kMaxCtas) ctas = kMaxCtas;
     if (ctas > most) ctas = most;
+    static std::atomic<unsigned> ready[2];
     auto kern = a.group <= 8 ? attend_kernel<T, D, 8> : attend_kernel<T, D, 16>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    cudaError_t e = allow_smem((const void*)kern, smem, ready[a.group <= 8 ? 0 : 1], dev);
     if (e == cudaSuccess) e = launch_pdl(true, kern, dim3((unsigned)ctas), dim3(kAttThreads), smem, st, a);
     // rows can only be cut where there are fewer rows than tiles
     if (e == cudaSuccess && ctas > 1 && most > rows) {

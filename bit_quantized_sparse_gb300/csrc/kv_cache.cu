@@ -375,8 +375,10 @@ int moe_w4_kv_evict(const moe_w4_kv_cache* c, const moe_w4_kv_track* track, cons
     a.kept = reinterpret_cast<int32_t*>(ws + MOE_W4_CTRL_BYTES + 2 * list);
     a.status = reinterpret_cast<unsigned int*>(ws);
     const size_t smem = (size_t)a.key_room * 4;
-    cudaError_t e = cudaFuncSetAttribute(kv_evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         kKeyRoom * 4);
+    static std::atomic<unsigned> ready;
+    int dev = 0;
+    if (sm_count(&dev) < 1) return MOE_W4_ERR_LAUNCH;
+    cudaError_t e = allow_smem((const void*)kv_evict_select_kernel, kKeyRoom * 4, ready, dev);
     if (e == cudaSuccess)
         e = launch_pdl(true, kv_evict_select_kernel, dim3((unsigned)rows), dim3(kSelectThreads), smem, stream, a);
     if (e == cudaSuccess) {

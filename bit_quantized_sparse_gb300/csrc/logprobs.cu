@@ -2,7 +2,24 @@
 // logits x:
 //   lse = m + log Z,  Z = sum exp(x - m),  m = max x
 //   logprob(t) = x_t - lse,  entropy = log Z - sum exp(x - m) (x - m) / Z
-// Every logit is read once in principle: HBM bounds large calls.
+//
+// HBM bounds large calls (each logit is read once; 16-bit logits arrive at about
+// 12 a clock and SM, and take one exponential and about six instructions
+// each), latency small ones.
+//
+// A row belongs to a cluster of 1 to 8 CTAs, each with a contiguous part; the
+// clusters of a resident grid take rows in turn.  A thread streams vectors of
+// 16 bytes through slots of shared memory that only it uses, so nothing but
+// its own copies is waited for, and the ring runs on into the next row while
+// the CTA finishes this one.  It keeps a reference maximum, Z and
+// U = sum e (x - m), and its largest logit.
+//
+// The top k of a part: the k-th largest of the threads' maxima is a lower bound
+// tau of the k-th largest logit, so only threads whose maximum reaches tau (k
+// of them, more with ties) read their vectors again, from L2, and list what
+// reaches it; the list, a few entries more than k, is sorted by warps.  Ties
+// at tau and NaN can make the list too long or too short: paths of their own
+// below, exact for every input.
 #include "serving.cuh"
 
 namespace mw4 {
@@ -19,85 +36,491 @@ struct LogprobArgs {
     unsigned int* status;
 };
 
-template <typename T> MW4_DEV float to_float(T v);
-template <> MW4_DEV float to_float<float>(float v) { return v; }
-template <> MW4_DEV float to_float<__nv_bfloat16>(__nv_bfloat16 v) { return __bfloat162float(v); }
-template <> MW4_DEV float to_float<__half>(__half v) { return __half2float(v); }
-
 // Order of the alternatives: larger logit first, then the lower index; NaN
 // after every number.  No logit has key 0.
 MW4_DEV uint32_t logit_key(float x) { return isnan(x) ? 1u : order_key(x + 0.f); }
 MW4_DEV uint64_t logit_word(float x, int i) { return ((uint64_t)logit_key(x) << 32) | (uint32_t)~i; }
 
-constexpr int kRowThreads = 1024;
+constexpr int kLpThreads = 256, kLpWarps = kLpThreads / 32;
+constexpr int kLpVecs = 2;                                // vectors of a thread in a stage
+constexpr int kLpStages = 5;
+constexpr int kLpChunk = kLpThreads * kLpVecs;            // vectors of a CTA in a stage
+constexpr int kLpSmem = kLpStages * kLpChunk * 16;
+constexpr int kLpCtas = 4;                                // resident CTAs per SM
+constexpr int kLpList = 512;                             // candidates listed before the paths for ties
+constexpr int kLpMaxCluster = 8;
+constexpr float kLpLazy = 5.5f;                           // growth of the maximum before a rescale
 
-template <typename V, typename F>
-MW4_DEV V block_reduce(V v, V* sh, F f) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+template <typename T> struct Logit;
+template <> struct Logit<float> {
+    static constexpr int E = 4;   // of a 16-byte vector
+    MW4_DEV static float one(const float* p) { return *p; }
+    MW4_DEV static void split(const uint4& v, float2 (&x)[2]) {
+        x[0] = make_float2(__uint_as_float(v.x), __uint_as_float(v.y));
+        x[1] = make_float2(__uint_as_float(v.z), __uint_as_float(v.w));
+    }
+};
+template <> struct Logit<__nv_bfloat16> {
+    static constexpr int E = 8;
+    MW4_DEV static float one(const __nv_bfloat16* p) { return __bfloat162float(*p); }
+    MW4_DEV static float2 two(uint32_t u) { return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u)); }
+    MW4_DEV static void split(const uint4& v, float2 (&x)[4]) { x[0] = two(v.x); x[1] = two(v.y); x[2] = two(v.z); x[3] = two(v.w); }
+};
+template <> struct Logit<__half> {
+    static constexpr int E = 8;
+    MW4_DEV static float one(const __half* p) { return __half2float(*p); }
+    MW4_DEV static float2 two(uint32_t u) { return __half22float2(*reinterpret_cast<__half2*>(&u)); }
+    MW4_DEV static void split(const uint4& v, float2 (&x)[4]) { x[0] = two(v.x); x[1] = two(v.y); x[2] = two(v.z); x[3] = two(v.w); }
+};
+
+// two fp32 operations in one instruction
+MW4_DEV uint64_t f2u(float2 v) { return *reinterpret_cast<uint64_t*>(&v); }
+MW4_DEV float2 u2f(uint64_t v) { return *reinterpret_cast<float2*>(&v); }
+MW4_DEV float2 add2(float2 a, float2 b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(f2u(a)), "l"(f2u(b)));
+    return u2f(d);
+}
+MW4_DEV float2 mul2(float2 a, float2 b) {
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(f2u(a)), "l"(f2u(b)));
+    return u2f(d);
+}
+MW4_DEV float2 fma2(float2 a, float2 b, float2 c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(f2u(a)), "l"(f2u(b)), "l"(f2u(c)));
+    return u2f(d);
+}
+MW4_DEV float max_keeping_nan(float a, float b) {
+    float d;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+    return d;
+}
+
+// Sums of a set of logits: Z = sum 2^y, U = sum 2^y y with y = (x - m) log2 e.
+// An empty set, or one of nothing but -inf, has m = -inf and Z = U = 0.
+struct Sums {
+    float m, Z, U;
+};
+MW4_DEV void rebase(Sums& s, float m) {   // m >= s.m
+    if (s.m == -INFINITY) {
+        // nothing to move (Z keeps a NaN)
+    } else if (m != s.m) {
+        const float y = (s.m - m) * kLog2e, f = ex2(y);
+        s.U = f == 0.f ? 0.f * s.Z : f * (s.U + s.Z * y);
+        s.Z *= f;
+    }
+    s.m = m;
+}
+MW4_DEV Sums warp_join(Sums s) {
+    float m = s.m;
 #pragma unroll
-    for (int off = 16; off; off >>= 1) v = f(v, __shfl_xor_sync(0xffffffffu, v, off));
-    __syncthreads();
-    if (lane == 0) sh[warp] = v;
-    __syncthreads();
-    v = sh[lane];
+    for (int off = 16; off; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+    rebase(s, m);
+    s.Z = warp_sum(s.Z);
+    s.U = warp_sum(s.U);
+    return s;
+}
+
+// Bitonic networks over a warp, largest in lane 0.
+template <typename V>
+MW4_DEV V warp_sort(V v) {
+    const int lane = threadIdx.x & 31;
 #pragma unroll
-    for (int off = 16; off; off >>= 1) v = f(v, __shfl_xor_sync(0xffffffffu, v, off));
+    for (int k = 2; k <= 32; k <<= 1)
+#pragma unroll
+        for (int j = k >> 1; j; j >>= 1) {
+            const V o = __shfl_xor_sync(0xffffffffu, v, j);
+            const bool larger = ((lane & j) == 0) == ((lane & k) == 0 || k == 32);
+            v = larger ? (o > v ? o : v) : (o > v ? v : o);
+        }
+    return v;
+}
+// The 32 largest of two sorted lists, sorted.
+template <typename V>
+MW4_DEV V warp_merge(V a, V b) {
+    const int lane = threadIdx.x & 31;
+    const V r = __shfl_sync(0xffffffffu, b, 31 - lane);
+    V v = r > a ? r : a;
+#pragma unroll
+    for (int j = 16; j; j >>= 1) {
+        const V o = __shfl_xor_sync(0xffffffffu, v, j);
+        v = (lane & j) == 0 ? (o > v ? o : v) : (o > v ? v : o);
+    }
     return v;
 }
 
-// One CTA per row.
+MW4_DEV uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+MW4_DEV uint32_t cluster_size() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+    return r;
+}
+MW4_DEV void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// Shared memory of CTA 0 of the cluster.
+MW4_DEV uint32_t at_rank0(const void* p) {
+    uint32_t a;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(a) : "r"(smem_u32(p)));
+    return a;
+}
+MW4_DEV void st_cluster(uint32_t a, uint64_t v) { asm volatile("st.shared::cluster.u64 [%0], %1;" :: "r"(a), "l"(v) : "memory"); }
+MW4_DEV void st_cluster(uint32_t a, float v) { asm volatile("st.shared::cluster.f32 [%0], %1;" :: "r"(a), "f"(v) : "memory"); }
+
+// A CTA's part of a row: vectors [v0, v1) of the row's 16-byte aligned body,
+// and for CTA 0 the logits before and after the body, one for each of the
+// first threads.
 template <typename T>
-__global__ void __launch_bounds__(kRowThreads) token_logprobs_kernel(const LogprobArgs a) {
-    __shared__ float sh_f[32];
-    __shared__ uint64_t sh_w[32];
-    griddep_wait();
-    const int row = blockIdx.x, tid = threadIdx.x;
-    const T* x = static_cast<const T*>(a.logits) + row * a.row_stride;
-    auto add = [](float p, float q) { return p + q; };
-    float m = -INFINITY;
-    int odd = 0;   // a NaN or +inf
-    for (int i = tid; i < a.vocab; i += kRowThreads) {
-        const float v = to_float(x[i]);
-        m = fmaxf(m, v);
-        odd |= isnan(v) || v == INFINITY;
+struct Part {
+    const T* row;
+    int head, v0, v1, scalar, count;   // scalar: this thread's logit outside the body, or -1; count: logits of the part
+    MW4_DEV Part(const LogprobArgs& a, int r, int rank, int ctas) {
+        constexpr int E = Logit<T>::E;
+        row = static_cast<const T*>(a.logits) + r * a.row_stride;
+        const int skew = (int)((reinterpret_cast<uintptr_t>(row) & 15) / sizeof(T));
+        head = min(skew ? E - skew : 0, a.vocab);
+        const int vecs = (a.vocab - head) / E, per = (vecs + ctas - 1) / ctas;
+        v0 = min(vecs, rank * per);
+        v1 = min(vecs, v0 + per);
+        const int rest = a.vocab - vecs * E;   // head and tail together
+        const int tid = threadIdx.x;
+        scalar = rank == 0 && tid < rest ? (tid < head ? tid : tid + vecs * E) : -1;
+        count = (v1 - v0) * E + (rank == 0 ? rest : 0);
     }
-    m = block_reduce(m, sh_f, [](float p, float q) { return fmaxf(p, q); });
-    odd = __syncthreads_or(odd);
-    float Z = 0.f, U = 0.f;
-    for (int i = tid; i < a.vocab; i += kRowThreads) {
-        const float d = fmaxf(to_float(x[i]) - m, -200.f);   // exp is 0 below about -104
-        const float e = __expf(d);
-        Z += e;
-        U += e * d;
-    }
-    Z = block_reduce(Z, sh_f, add);
-    U = block_reduce(U, sh_f, add);
-    const bool none = odd || m == -INFINITY;
-    const float lse = none ? NAN : m + logf(Z);
-    if (tid == 0) {
-        if (a.entropy) a.entropy[row] = none ? NAN : logf(Z) - U / Z;
-        if (a.targets) {
-            const int t = a.targets[row];
-            const bool in = (unsigned)t < (unsigned)a.vocab;
-            if (!in && t != -1) raise_status(a.status, MOE_W4_STATUS_BAD_INDEX);
-            a.logprob[row] = in ? to_float(x[t]) - lse : t == -1 ? 0.f : NAN;
-        }
-    }
-    uint64_t last = ~0ull;
-    for (int k = 0; k < a.top; ++k) {
+    MW4_DEV int chunks() const { return max(1, (v1 - v0 + kLpChunk - 1) / kLpChunk); }
+    MW4_DEV const uint4* vec(int v) const { return reinterpret_cast<const uint4*>(row + head) + v; }
+    MW4_DEV int index(int v) const { return head + v * Logit<T>::E; }
+};
+
+struct LpShared {
+    float lane_max[kLpWarps][32];
+    uint64_t sorted[kLpWarps][32];
+    uint64_t list[kLpList];
+    uint64_t part_words[2][kLpMaxCluster][32];   // of the cluster's CTAs, in CTA 0; by turns
+    float part_sums[2][kLpMaxCluster][3];
+    Sums sums[kLpWarps];
+    int warp_count[kLpWarps];
+    int count;
+    float tau;
+};
+
+// The kk largest words of a part by kk rounds over it.  Only for parts whose
+// list is too long for another reason than ties, or short of kk because of NaN.
+template <typename T>
+MW4_DEV uint64_t top_by_rounds(const Part<T>& p, int kk, LpShared& sh) {
+    constexpr int E = Logit<T>::E;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    uint64_t last = ~0ull, mine = 0;
+    for (int k = 0; k < kk; ++k) {
         uint64_t best = 0;
-        for (int i = tid; i < a.vocab; i += kRowThreads) {
-            const uint64_t w = logit_word(to_float(x[i]), i);
+        auto see = [&](float x, int i) {
+            const uint64_t w = logit_word(x, i);
             if (w < last && w > best) best = w;
+        };
+        if (p.scalar >= 0) see(Logit<T>::one(p.row + p.scalar), p.scalar);
+        for (int v = p.v0 + tid; v < p.v1; v += kLpThreads) {
+            float2 x[E / 2];
+            Logit<T>::split(*p.vec(v), x);
+            for (int j = 0; j < E / 2; ++j) {
+                see(x[j].x, p.index(v) + 2 * j);
+                see(x[j].y, p.index(v) + 2 * j + 1);
+            }
         }
-        best = block_reduce(best, sh_w, [](uint64_t p, uint64_t q) { return p > q ? p : q; });
-        if (tid == 0) {
-            const int i = (int)~(uint32_t)best;
-            a.top_index[(int64_t)row * a.top + k] = i;
-            a.top_logprob[(int64_t)row * a.top + k] = to_float(x[i]) - lse;
+#pragma unroll
+        for (int off = 16; off; off >>= 1) {
+            const uint64_t o = __shfl_xor_sync(0xffffffffu, best, off);
+            best = o > best ? o : best;
         }
+        __syncthreads();
+        if (lane == 0) sh.sorted[warp][0] = best;
+        __syncthreads();
+        for (int w = 0; w < kLpWarps; ++w) best = sh.sorted[w][0] > best ? sh.sorted[w][0] : best;
+        if (lane == k) mine = best;
         last = best;
     }
+    return mine;
+}
+
+// Lists the logits of the part that are >= tau (> tau where strict).
+template <typename T>
+MW4_DEV void list_from(const Part<T>& p, float thread_max, float tau, bool strict, LpShared& sh) {
+    constexpr int E = Logit<T>::E;
+    if (!(strict ? thread_max > tau : thread_max >= tau)) return;
+    auto see = [&](float x, int i) {
+        if (strict ? x > tau : x >= tau) {
+            const int at = atomicAdd(&sh.count, 1);
+            if (at < kLpList) sh.list[at] = logit_word(x, i);
+        }
+    };
+    if (p.scalar >= 0) see(Logit<T>::one(p.row + p.scalar), p.scalar);
+#pragma unroll 4
+    for (int v = p.v0 + (int)threadIdx.x; v < p.v1; v += kLpThreads) {
+        float2 x[E / 2];
+        Logit<T>::split(*p.vec(v), x);
+#pragma unroll
+        for (int j = 0; j < E / 2; ++j) {
+            see(x[j].x, p.index(v) + 2 * j);
+            see(x[j].y, p.index(v) + 2 * j + 1);
+        }
+    }
+}
+
+// Adds to the list the `need` lowest-indexed logits of the body that equal tau
+// (fewer if there are not so many), and all such logits outside it (at most 14).
+template <typename T>
+MW4_DEV void list_ties(const Part<T>& p, float tau, int need, LpShared& sh) {
+    constexpr int E = Logit<T>::E;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (p.scalar >= 0) {
+        const float x = Logit<T>::one(p.row + p.scalar);
+        if (x == tau) sh.list[atomicAdd(&sh.count, 1)] = logit_word(x, p.scalar);
+    }
+    for (int base = p.v0; base < p.v1 && need > 0; base += kLpThreads) {
+        const int v = base + tid;
+        float2 x[E / 2];
+        uint32_t eq = 0;
+        if (v < p.v1) {
+            Logit<T>::split(*p.vec(v), x);
+#pragma unroll
+            for (int j = 0; j < E / 2; ++j) eq |= (uint32_t)(x[j].x == tau) << (2 * j) | (uint32_t)(x[j].y == tau) << (2 * j + 1);
+        }
+        const int mine = __popc(eq);
+        int incl = mine;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const int o = __shfl_up_sync(0xffffffffu, incl, off);
+            if (lane >= off) incl += o;
+        }
+        __syncthreads();
+        if (lane == 31) sh.warp_count[warp] = incl;
+        __syncthreads();
+        int before = incl - mine, all = 0;
+        for (int w = 0; w < kLpWarps; ++w) {
+            before += w < warp ? sh.warp_count[w] : 0;
+            all += sh.warp_count[w];
+        }
+        for (; eq && before < need; eq &= eq - 1, ++before)
+            sh.list[atomicAdd(&sh.count, 1)] = logit_word(tau, p.index(v) + __ffs(eq) - 1);
+        need -= all;
+    }
+}
+
+// The kk largest words of a part, in lanes 0.. of warp 0.
+template <typename T>
+MW4_DEV uint64_t part_top(const Part<T>& p, float thread_max, int kk, LpShared& sh) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    sh.lane_max[warp][lane] = warp_sort(thread_max);
+    if (tid == 0) sh.count = 0;
+    __syncthreads();
+    if (warp == 0) {
+        float v = sh.lane_max[0][lane];
+#pragma unroll
+        for (int w = 1; w < kLpWarps; ++w) v = warp_merge(v, sh.lane_max[w][lane]);
+        if (lane == kk - 1) sh.tau = v;
+    }
+    __syncthreads();
+    const float tau = sh.tau;
+    list_from(p, thread_max, tau, false, sh);
+    __syncthreads();
+    int c = sh.count;
+    if (c > kLpList) {   // many ties at tau: what exceeds it, then the first of them
+        __syncthreads();
+        if (tid == 0) sh.count = 0;
+        __syncthreads();
+        list_from(p, thread_max, tau, true, sh);
+        __syncthreads();
+        c = sh.count;
+        __syncthreads();
+        if (c <= kLpList && c < kk) {
+            list_ties(p, tau, kk - c, sh);
+            __syncthreads();
+            c = sh.count;
+        }
+    }
+    if (c > kLpList || c < kk) return top_by_rounds(p, kk, sh);
+    const int lists = min(kLpWarps, (c + 31) / 32);
+    uint64_t best = 0;
+    if (warp < lists) {
+        for (int at = warp * 32; at < c; at += kLpThreads) {
+            const uint64_t s = warp_sort(at + lane < c ? sh.list[at + lane] : 0ull);
+            best = at == warp * 32 ? s : warp_merge(best, s);
+        }
+        sh.sorted[warp][lane] = best;
+    }
+    if (lists > 1) {
+        __syncthreads();
+        if (warp == 0)
+            for (int w = 1; w < lists; ++w) best = warp_merge(best, sh.sorted[w][lane]);
+    }
+    return lane < kk ? best : 0ull;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kLpThreads, kLpCtas) token_logprobs_kernel(const LogprobArgs a) {
+    extern __shared__ __align__(16) uint4 ring[];
+    __shared__ LpShared sh;
+    constexpr int E = Logit<T>::E;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int rank = (int)cluster_rank(), ctas = (int)cluster_size();
+    const int first = blockIdx.x / ctas, step = gridDim.x / ctas;
+    griddep_wait();
+
+    // the place that is loaded next: a chunk of a row
+    int load_row = first, load_chunk = 0;
+    auto load = [&](int stage) {
+        if (load_row < a.n) {
+            const Part<T> p(a, load_row, rank, ctas);
+            const int v0 = p.v0 + load_chunk * kLpChunk + tid;
+#pragma unroll
+            for (int i = 0; i < kLpVecs; ++i)
+                if (v0 + i * kLpThreads < p.v1)
+                    cp_async_16(&ring[stage * kLpChunk + i * kLpThreads + tid], p.vec(v0 + i * kLpThreads));
+            if (++load_chunk == p.chunks()) {
+                load_chunk = 0;
+                load_row += step;
+            }
+        }
+        cp_async_commit();
+    };
+#pragma unroll
+    for (int i = 0; i < kLpStages - 1; ++i) load(i);
+
+    int stage = 0, turn = 0;
+    for (int r = first; r < a.n; r += step, turn ^= 1) {
+        const Part<T> p(a, r, rank, ctas);
+        float scalar = -INFINITY;
+        if (p.scalar >= 0) scalar = Logit<T>::one(p.row + p.scalar);
+        Sums s{-INFINITY, 0.f, 0.f};
+        float most = -INFINITY;
+        float2 Z = make_float2(0.f, 0.f), U = Z;
+        const int chunks = p.chunks();
+        for (int c = 0; c < chunks; ++c) {
+            cp_async_wait<kLpStages - 2>();
+            load(stage == 0 ? kLpStages - 1 : stage - 1);
+            const int v0 = p.v0 + c * kLpChunk + tid;
+#pragma unroll
+            for (int i = 0; i < kLpVecs; ++i) {
+                if (v0 + i * kLpThreads >= p.v1) break;
+                float2 x[E / 2];
+                Logit<T>::split(ring[stage * kLpChunk + i * kLpThreads + tid], x);
+                float vm = fmaxf(x[0].x, x[0].y);
+#pragma unroll
+                for (int j = 1; j < E / 2; ++j) vm = fmaxf(vm, fmaxf(x[j].x, x[j].y));
+                most = fmaxf(most, vm);
+                // The reference follows the maximum when that has outgrown it by more than
+                // kLpLazy, so that a rescale is rare; the sums stay far inside fp32's range.
+                if (vm > s.m + kLpLazy || (s.m == -INFINITY && vm > -INFINITY)) {
+                    Sums t{s.m, Z.x + Z.y, U.x + U.y};
+                    rebase(t, vm);
+                    s.m = vm;
+                    Z = make_float2(t.Z, 0.f);
+                    U = make_float2(t.U, 0.f);
+                }
+                const float ref = s.m == -INFINITY ? 0.f : s.m;
+                const float2 minus = make_float2(-ref, -ref), l2e = make_float2(kLog2e, kLog2e);
+#pragma unroll
+                for (int j = 0; j < E / 2; ++j) {
+                    float2 y = mul2(add2(x[j], minus), l2e);
+                    // 2^-200 is 0: keeps 0 * -inf out of U; a NaN stays
+                    y = make_float2(max_keeping_nan(y.x, -200.f), max_keeping_nan(y.y, -200.f));
+                    const float2 e = make_float2(ex2(y.x), ex2(y.y));
+                    Z = add2(Z, e);
+                    U = fma2(e, y, U);
+                }
+            }
+            stage = stage == kLpStages - 1 ? 0 : stage + 1;
+        }
+        s.Z = Z.x + Z.y;
+        s.U = U.x + U.y;
+        if (p.scalar >= 0) {
+            if (scalar > s.m) rebase(s, scalar);
+            const float y = max_keeping_nan((scalar - (s.m == -INFINITY ? 0.f : s.m)) * kLog2e, -200.f), e = ex2(y);
+            s.Z += e;
+            s.U += e * y;
+            most = fmaxf(most, scalar);
+        }
+        s = warp_join(s);
+        if (lane == 0) sh.sums[warp] = s;
+        uint64_t word = 0;
+        const int kk = min(a.top, p.count);
+        if (kk) word = part_top(p, most, kk, sh);
+        else __syncthreads();
+        if (warp == 0) {
+            s = warp_join(lane < kLpWarps ? sh.sums[lane] : Sums{-INFINITY, 0.f, 0.f});
+            if (ctas > 1) {
+                st_cluster(at_rank0(&sh.part_words[turn][rank][lane]), word);
+                if (lane < 3) st_cluster(at_rank0(&sh.part_sums[turn][rank][lane]), lane == 0 ? s.m : lane == 1 ? s.Z : s.U);
+            }
+        }
+        if (ctas > 1) cluster_sync();
+        else __syncthreads();
+        if (rank == 0 && warp == 0) {
+            if (ctas > 1) {
+                const float* q = sh.part_sums[turn][lane < ctas ? lane : 0];
+                s = warp_join(lane < ctas ? Sums{q[0], q[1], q[2]} : Sums{-INFINITY, 0.f, 0.f});
+                if (a.top)
+                    for (int c = 1; c < ctas; ++c) word = warp_merge(word, sh.part_words[turn][c][lane]);
+            }
+            // a NaN, +inf (x - m is NaN then), or nothing but -inf
+            const bool none = s.m == -INFINITY || isnan(s.Z);
+            const float logZ = log2f(s.Z) * kLn2;
+            const float lse = none ? NAN : s.m + logZ;
+            if (lane < a.top) {
+                const int i = (int)~(uint32_t)word;
+                a.top_index[(int64_t)r * a.top + lane] = i;
+                a.top_logprob[(int64_t)r * a.top + lane] = Logit<T>::one(p.row + i) - lse;
+            }
+            if (lane == 0) {
+                if (a.entropy) a.entropy[r] = none ? NAN : logZ - s.U / s.Z * kLn2;
+                if (a.targets) {
+                    const int t = a.targets[r];
+                    const bool in = (unsigned)t < (unsigned)a.vocab;
+                    if (!in && t != -1) raise_status(a.status, MOE_W4_STATUS_BAD_INDEX);
+                    a.logprob[r] = in ? Logit<T>::one(p.row + t) - lse : t == -1 ? 0.f : NAN;
+                }
+            }
+        }
+    }
+}
+
+// CTAs of a row: as many (up to 8) as keep every SM's places filled at most once
+// and leave each CTA a stage's worth of vectors or more.
+static int row_ctas(int n, int64_t vecs, int places) {
+    int c = 1;
+    while (c < kLpMaxCluster && (int64_t)n * c * 2 <= places && vecs >= (int64_t)kLpChunk / 2 * c * 2) c *= 2;
+    return c;
+}
+
+template <typename T>
+static cudaError_t launch_logprobs(const LogprobArgs& a, cudaStream_t st) {
+    int dev = 0;
+    const int sms = sm_count(&dev);
+    if (sms < 1) return cudaErrorInvalidDevice;
+    static std::atomic<unsigned> ready;
+    cudaError_t e = allow_smem((const void*)token_logprobs_kernel<T>, kLpSmem, ready, dev);
+    if (e != cudaSuccess) return e;
+    const int places = sms * kLpCtas;
+    const int ctas = row_ctas(a.n, a.vocab / Logit<T>::E, places);
+    const int clusters = a.n < places / ctas ? a.n : places / ctas;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = ctas;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)(clusters * ctas));
+    cfg.blockDim = dim3(kLpThreads);
+    cfg.dynamicSmemBytes = kLpSmem;
+    cfg.stream = st;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, token_logprobs_kernel<T>, a);
 }
 
 }  // namespace mw4
@@ -120,9 +543,8 @@ extern "C" int moe_w4_token_logprobs(int dtype, int n, int vocab, const void* lo
         return MOE_W4_ERR_ALIGN;
     const int r = check_workspace(workspace, ws_bytes, MOE_W4_CTRL_BYTES);
     if (r) return r;
-    LogprobArgs a{logits, row_stride, n, vocab, top, targets, logprob, entropy, top_index, top_logprob,
-                  static_cast<unsigned int*>(workspace)};
-    auto kern = dtype == MOE_W4_TYPE_BF16 ? token_logprobs_kernel<__nv_bfloat16>
-                : dtype == MOE_W4_TYPE_FP16 ? token_logprobs_kernel<__half> : token_logprobs_kernel<float>;
-    return launched(launch_pdl(true, kern, dim3(n), dim3(kRowThreads), 0, stream, a));
+    const LogprobArgs a{logits, row_stride, n, vocab, top, targets, logprob, entropy, top_index, top_logprob,
+                        static_cast<unsigned int*>(workspace)};
+    return launched(dtype == MOE_W4_TYPE_BF16 ? launch_logprobs<__nv_bfloat16>(a, stream)
+                    : dtype == MOE_W4_TYPE_FP16 ? launch_logprobs<__half>(a, stream) : launch_logprobs<float>(a, stream));
 }

@@ -1,6 +1,8 @@
 // Shared by the operators of moe_w4_serving.h: the cache as the kernels see it,
 // argument checks, exact division by a page size, and element types.
 #pragma once
+#include <atomic>
+
 #include "common.cuh"
 #include "internal.h"
 #include "moe_w4_serving.h"
@@ -43,6 +45,13 @@ MW4_DEV int64_t kv_offset(const KvView& c, int b, int t) {
     return page * c.page_stride + (int64_t)(t - p * c.page.d) * c.slot_stride;
 }
 
+MW4_DEV float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+constexpr float kLn2 = 0.693147180559945309f, kLog2e = 1.44269504088896341f;
+
 inline bool misaligned(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) != 0; }
 
 inline int check_cache(const moe_w4_kv_cache* c, bool need_lens) {
@@ -80,6 +89,28 @@ inline KvView kv_view(const moe_w4_kv_cache& c) {
 }
 
 inline size_t round_up(size_t v, size_t to) { return (v + to - 1) / to * to; }
+
+// The current device and its SM count (asked once per device).
+inline int sm_count(int* device = nullptr) {
+    static std::atomic<int> cached[16];
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0) return 0;
+    if (device) *device = dev;
+    if (dev < 16 && (n = cached[dev].load(std::memory_order_relaxed))) return n;
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+    if (dev < 16) cached[dev].store(n, std::memory_order_relaxed);
+    return n;
+}
+
+// Lets a kernel take `bytes` of dynamic shared memory; the runtime is asked once
+// per device.  `done` belongs to the kernel.
+inline cudaError_t allow_smem(const void* kern, int bytes, std::atomic<unsigned>& done, int dev) {
+    const unsigned bit = dev < 32 ? 1u << dev : 0u;
+    if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+    return e;
+}
 
 inline int launched(cudaError_t e) {
     if (e == cudaSuccess) return MOE_W4_OK;

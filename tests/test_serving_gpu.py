@@ -424,7 +424,7 @@ def test_logprobs_strided_rows(torch, sv, dtype, offset):
 
 @pytest.mark.parametrize("dtype", ["float32", "bfloat16", "float16"])
 @pytest.mark.parametrize("kind", ["equal", "ascending", "descending", "masked", "lowest", "one", "peak", "two_values", "odd",
-                                  "minus_zero"])
+                                  "minus_zero", "periodic"])
 @pytest.mark.parametrize("vocab", [200, 20003, 140001])
 def test_logprobs_odd_rows(torch, sv, dtype, kind, vocab):
     dt = getattr(torch, dtype)
@@ -453,6 +453,8 @@ def test_logprobs_odd_rows(torch, sv, dtype, kind, vocab):
         x[0, 5], x[1, vocab - 3], x[2, 9] = float("nan"), float("inf"), float("-inf")
         x[3].fill_(float("nan"))
         x[3, 4] = 1.0
+    elif kind == "periodic":    # a few threads of a block hold all the large logits
+        x += torch.where(torch.arange(vocab, device="cuda") % (1024 if dtype == "float32" else 2048) < 120, 20, 0).to(dt)
     else:
         x.copy_(torch.where(x > 0, torch.zeros_like(x), -torch.zeros_like(x)))
     check_logprobs(torch, sv, x, torch.tensor([0, vocab - 1, vocab // 2, 17], dtype=torch.int32, device="cuda"), 20)
@@ -510,3 +512,13 @@ def test_refusals_leave_no_work(torch, sv):
         sv.token_logprobs(torch.zeros(2, 9, device="cuda").t())
     with pytest.raises(MoeW4Error):
         sv.token_logprobs(torch.zeros(2, 9, device="cuda"), top=10)
+
+
+@pytest.mark.parametrize("rows", [200, 700])
+def test_logprobs_many_rows(torch, sv, rows):
+    """More rows than the grid has places: CTAs and clusters take several in turn."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(rows)
+    x = (torch.randn(rows, 5003, device="cuda", generator=g) * 3).to(torch.bfloat16)
+    t = torch.randint(0, 5003, (rows,), device="cuda", generator=g).to(torch.int32)
+    check_logprobs(torch, sv, x, t, 9)
