@@ -39,11 +39,14 @@ struct LogprobArgs {
 // Order of the alternatives: larger logit first, then the lower index; NaN
 // after every number.  No logit has key 0.
 MW4_DEV uint32_t logit_key(float x) { return isnan(x) ? 1u : order_key(x + 0.f); }
+MW4_DEV float key_logit(uint32_t k) {
+    return k == 1u ? NAN : __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
+}
 MW4_DEV uint64_t logit_word(float x, int i) { return ((uint64_t)logit_key(x) << 32) | (uint32_t)~i; }
 
 constexpr int kLpThreads = 256, kLpWarps = kLpThreads / 32;
-constexpr int kLpVecs = 2;                                // vectors of a thread in a stage
-constexpr int kLpStages = 5;
+constexpr int kLpVecs = 3;                                // vectors of a thread in a stage
+constexpr int kLpStages = 3;
 constexpr int kLpChunk = kLpThreads * kLpVecs;            // vectors of a CTA in a stage
 constexpr int kLpSmem = kLpStages * kLpChunk * 16;
 constexpr int kLpCtas = 4;                                // resident CTAs per SM
@@ -95,6 +98,18 @@ MW4_DEV float max_keeping_nan(float a, float b) {
     float d;
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
     return d;
+}
+
+MW4_DEV float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+template <int N>
+MW4_DEV float max_of(const float2 (&x)[N]) {
+    float v = max3(x[0].x, x[0].y, x[1].x), w = x[1].y;
+    if (N == 4) w = max3(max3(x[1].y, x[2 % N].x, x[2 % N].y), x[3 % N].x, x[3 % N].y);
+    return fmaxf(v, w);
 }
 
 // Sums of a set of logits: Z = sum 2^y, U = sum 2^y y with y = (x - m) log2 e.
@@ -246,26 +261,31 @@ MW4_DEV uint64_t top_by_rounds(const Part<T>& p, int kk, LpShared& sh) {
     return mine;
 }
 
-// Lists the logits of the part that are >= tau (> tau where strict).
+// Lists the logits of the part that are >= tau (> tau where strict).  The warp
+// reads the vectors of one thread after the other that has such a logit.
 template <typename T>
-MW4_DEV void list_from(const Part<T>& p, float thread_max, float tau, bool strict, LpShared& sh) {
+MW4_DEV void list_from(const Part<T>& p, float thread_max, float scalar, float tau, bool strict, LpShared& sh) {
     constexpr int E = Logit<T>::E;
-    if (!(strict ? thread_max > tau : thread_max >= tau)) return;
+    const int lane = threadIdx.x & 31;
     auto see = [&](float x, int i) {
         if (strict ? x > tau : x >= tau) {
             const int at = atomicAdd(&sh.count, 1);
             if (at < kLpList) sh.list[at] = logit_word(x, i);
         }
     };
-    if (p.scalar >= 0) see(Logit<T>::one(p.row + p.scalar), p.scalar);
-#pragma unroll 4
-    for (int v = p.v0 + (int)threadIdx.x; v < p.v1; v += kLpThreads) {
-        float2 x[E / 2];
-        Logit<T>::split(*p.vec(v), x);
+    if (p.scalar >= 0) see(scalar, p.scalar);
+    for (uint32_t hits = __ballot_sync(0xffffffffu, strict ? thread_max > tau : thread_max >= tau); hits; hits &= hits - 1) {
+        const int owner = (int)(threadIdx.x & ~31u) + __ffs(hits) - 1;
+        for (int v = p.v0 + owner + lane * kLpThreads; v < p.v1; v += 32 * kLpThreads) {
+            float2 x[E / 2];
+            Logit<T>::split(*p.vec(v), x);
+            if (max_of(x) >= tau) {
 #pragma unroll
-        for (int j = 0; j < E / 2; ++j) {
-            see(x[j].x, p.index(v) + 2 * j);
-            see(x[j].y, p.index(v) + 2 * j + 1);
+                for (int j = 0; j < E / 2; ++j) {
+                    see(x[j].x, p.index(v) + 2 * j);
+                    see(x[j].y, p.index(v) + 2 * j + 1);
+                }
+            }
         }
     }
 }
@@ -312,27 +332,29 @@ MW4_DEV void list_ties(const Part<T>& p, float tau, int need, LpShared& sh) {
 
 // The kk largest words of a part, in lanes 0.. of warp 0.
 template <typename T>
-MW4_DEV uint64_t part_top(const Part<T>& p, float thread_max, int kk, LpShared& sh) {
+MW4_DEV uint64_t part_top(const Part<T>& p, float thread_max, float scalar, int kk, LpShared& sh) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     sh.lane_max[warp][lane] = warp_sort(thread_max);
     if (tid == 0) sh.count = 0;
-    __syncthreads();
-    if (warp == 0) {
-        float v = sh.lane_max[0][lane];
 #pragma unroll
-        for (int w = 1; w < kLpWarps; ++w) v = warp_merge(v, sh.lane_max[w][lane]);
-        if (lane == kk - 1) sh.tau = v;
+    for (int half = kLpWarps / 2; half; half >>= 1) {
+        __syncthreads();
+        if (warp < half) {
+            const float v = warp_merge(sh.lane_max[warp][lane], sh.lane_max[warp + half][lane]);
+            if (half > 1) sh.lane_max[warp][lane] = v;
+            else if (lane == kk - 1) sh.tau = v;
+        }
     }
     __syncthreads();
     const float tau = sh.tau;
-    list_from(p, thread_max, tau, false, sh);
+    list_from(p, thread_max, scalar, tau, false, sh);
     __syncthreads();
     int c = sh.count;
     if (c > kLpList) {   // many ties at tau: what exceeds it, then the first of them
         __syncthreads();
         if (tid == 0) sh.count = 0;
         __syncthreads();
-        list_from(p, thread_max, tau, true, sh);
+        list_from(p, thread_max, scalar, tau, true, sh);
         __syncthreads();
         c = sh.count;
         __syncthreads();
@@ -370,19 +392,28 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas) token_logprobs_kernel(con
     const int first = blockIdx.x / ctas, step = gridDim.x / ctas;
     griddep_wait();
 
-    // the place that is loaded next: a chunk of a row
-    int load_row = first, load_chunk = 0;
-    auto load = [&](int stage) {
+    // the next vector of this thread to load, and how many of its row are left
+    int load_row = first, left = 0;
+    const uint4* from = nullptr;
+    auto load_part = [&]() {
         if (load_row < a.n) {
             const Part<T> p(a, load_row, rank, ctas);
-            const int v0 = p.v0 + load_chunk * kLpChunk + tid;
+            from = p.vec(p.v0 + tid);
+            left = p.v1 - p.v0 - tid;   // of the part, from this thread's on
+        }
+    };
+    load_part();
+    auto load = [&](int stage) {
+        if (load_row < a.n) {
+            uint4* to = &ring[stage * kLpChunk + tid];
 #pragma unroll
             for (int i = 0; i < kLpVecs; ++i)
-                if (v0 + i * kLpThreads < p.v1)
-                    cp_async_16(&ring[stage * kLpChunk + i * kLpThreads + tid], p.vec(v0 + i * kLpThreads));
-            if (++load_chunk == p.chunks()) {
-                load_chunk = 0;
+                if (left > i * kLpThreads) cp_async_16(to + i * kLpThreads, from + i * kLpThreads);
+            from += kLpChunk;
+            left -= kLpChunk;
+            if (left + tid <= 0) {   // the part is done: on to the next row's
                 load_row += step;
+                load_part();
             }
         }
         cp_async_commit();
@@ -395,34 +426,39 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas) token_logprobs_kernel(con
         const Part<T> p(a, r, rank, ctas);
         float scalar = -INFINITY;
         if (p.scalar >= 0) scalar = Logit<T>::one(p.row + p.scalar);
+        // what the end of the row needs from memory, asked for now
+        int target = -1;
+        float target_x = NAN;
+        if (rank == 0 && tid == 0 && a.targets) {
+            target = a.targets[r];
+            if ((unsigned)target < (unsigned)a.vocab) target_x = Logit<T>::one(p.row + target);
+        }
         Sums s{-INFINITY, 0.f, 0.f};
-        float most = -INFINITY;
-        float2 Z = make_float2(0.f, 0.f), U = Z;
-        const int chunks = p.chunks();
-        for (int c = 0; c < chunks; ++c) {
+        float most = -INFINITY, limit = -INFINITY;
+        float2 Z = make_float2(0.f, 0.f), U = Z, minus = Z;
+        for (int rest = p.v1 - p.v0 - tid, chunks = p.chunks(); chunks; --chunks, rest -= kLpChunk) {
             cp_async_wait<kLpStages - 2>();
             load(stage == 0 ? kLpStages - 1 : stage - 1);
-            const int v0 = p.v0 + c * kLpChunk + tid;
+            const uint4* at = &ring[stage * kLpChunk + tid];
 #pragma unroll
             for (int i = 0; i < kLpVecs; ++i) {
-                if (v0 + i * kLpThreads >= p.v1) break;
+                if (rest <= i * kLpThreads) break;
                 float2 x[E / 2];
-                Logit<T>::split(ring[stage * kLpChunk + i * kLpThreads + tid], x);
-                float vm = fmaxf(x[0].x, x[0].y);
-#pragma unroll
-                for (int j = 1; j < E / 2; ++j) vm = fmaxf(vm, fmaxf(x[j].x, x[j].y));
+                Logit<T>::split(at[i * kLpThreads], x);
+                const float vm = max_of(x);
                 most = fmaxf(most, vm);
                 // The reference follows the maximum when that has outgrown it by more than
                 // kLpLazy, so that a rescale is rare; the sums stay far inside fp32's range.
-                if (vm > s.m + kLpLazy || (s.m == -INFINITY && vm > -INFINITY)) {
+                if (vm > limit) {
                     Sums t{s.m, Z.x + Z.y, U.x + U.y};
                     rebase(t, vm);
                     s.m = vm;
+                    limit = vm + kLpLazy;
+                    minus = make_float2(-vm, -vm);
                     Z = make_float2(t.Z, 0.f);
                     U = make_float2(t.U, 0.f);
                 }
-                const float ref = s.m == -INFINITY ? 0.f : s.m;
-                const float2 minus = make_float2(-ref, -ref), l2e = make_float2(kLog2e, kLog2e);
+                const float2 l2e = make_float2(kLog2e, kLog2e);
 #pragma unroll
                 for (int j = 0; j < E / 2; ++j) {
                     float2 y = mul2(add2(x[j], minus), l2e);
@@ -448,7 +484,7 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas) token_logprobs_kernel(con
         if (lane == 0) sh.sums[warp] = s;
         uint64_t word = 0;
         const int kk = min(a.top, p.count);
-        if (kk) word = part_top(p, most, kk, sh);
+        if (kk) word = part_top(p, most, scalar, kk, sh);
         else __syncthreads();
         if (warp == 0) {
             s = warp_join(lane < kLpWarps ? sh.sums[lane] : Sums{-INFINITY, 0.f, 0.f});
@@ -471,17 +507,15 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas) token_logprobs_kernel(con
             const float logZ = log2f(s.Z) * kLn2;
             const float lse = none ? NAN : s.m + logZ;
             if (lane < a.top) {
-                const int i = (int)~(uint32_t)word;
-                a.top_index[(int64_t)r * a.top + lane] = i;
-                a.top_logprob[(int64_t)r * a.top + lane] = Logit<T>::one(p.row + i) - lse;
+                a.top_index[(int64_t)r * a.top + lane] = (int)~(uint32_t)word;
+                a.top_logprob[(int64_t)r * a.top + lane] = key_logit((uint32_t)(word >> 32)) - lse;
             }
             if (lane == 0) {
                 if (a.entropy) a.entropy[r] = none ? NAN : logZ - s.U / s.Z * kLn2;
                 if (a.targets) {
-                    const int t = a.targets[r];
-                    const bool in = (unsigned)t < (unsigned)a.vocab;
-                    if (!in && t != -1) raise_status(a.status, MOE_W4_STATUS_BAD_INDEX);
-                    a.logprob[r] = in ? Logit<T>::one(p.row + t) - lse : t == -1 ? 0.f : NAN;
+                    const bool in = (unsigned)target < (unsigned)a.vocab;
+                    if (!in && target != -1) raise_status(a.status, MOE_W4_STATUS_BAD_INDEX);
+                    a.logprob[r] = in ? target_x - lse : target == -1 ? 0.f : NAN;
                 }
             }
         }
