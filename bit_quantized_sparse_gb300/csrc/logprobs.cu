@@ -44,13 +44,10 @@ MW4_DEV float key_logit(uint32_t k) {
 }
 MW4_DEV uint64_t logit_word(float x, int i) { return ((uint64_t)logit_key(x) << 32) | (uint32_t)~i; }
 
-constexpr int kLpThreads = 256, kLpWarps = kLpThreads / 32;
 constexpr int kLpVecs = 3;                                // vectors of a thread in a stage
 constexpr int kLpStages = 3;
-constexpr int kLpChunk = kLpThreads * kLpVecs;            // vectors of a CTA in a stage
-constexpr int kLpSmem = kLpStages * kLpChunk * 16;
-constexpr int kLpCtas = 4;                                // resident CTAs per SM
-constexpr int kLpList = 512;                             // candidates listed before the paths for ties
+constexpr int kLpPerSm = 1024;                            // resident threads per SM
+constexpr int kLpList = 256;                              // candidates listed before the paths for ties
 constexpr int kLpMaxCluster = 8;
 constexpr float kLpLazy = 5.5f;                           // growth of the maximum before a rescale
 
@@ -190,7 +187,7 @@ MW4_DEV void st_cluster(uint32_t a, float v) { asm volatile("st.shared::cluster.
 // A CTA's part of a row: vectors [v0, v1) of the row's 16-byte aligned body,
 // and for CTA 0 the logits before and after the body, one for each of the
 // first threads.
-template <typename T>
+template <typename T, int NT>
 struct Part {
     const T* row;
     int head, v0, v1, scalar, count;   // scalar: this thread's logit outside the body, or -1; count: logits of the part
@@ -207,27 +204,28 @@ struct Part {
         scalar = rank == 0 && tid < rest ? (tid < head ? tid : tid + vecs * E) : -1;
         count = (v1 - v0) * E + (rank == 0 ? rest : 0);
     }
-    MW4_DEV int chunks() const { return max(1, (v1 - v0 + kLpChunk - 1) / kLpChunk); }
+    MW4_DEV int chunks() const { return max(1, (v1 - v0 + (NT * kLpVecs) - 1) / (NT * kLpVecs)); }
     MW4_DEV const uint4* vec(int v) const { return reinterpret_cast<const uint4*>(row + head) + v; }
     MW4_DEV int index(int v) const { return head + v * Logit<T>::E; }
 };
 
+template <int NT>
 struct LpShared {
-    float lane_max[kLpWarps][32];
-    uint64_t sorted[kLpWarps][32];
+    float lane_max[NT / 32][32];
+    uint64_t sorted[NT / 32][32];
     uint64_t list[kLpList];
     uint64_t part_words[2][kLpMaxCluster][32];   // of the cluster's CTAs, in CTA 0; by turns
     float part_sums[2][kLpMaxCluster][3];
-    Sums sums[kLpWarps];
-    int warp_count[kLpWarps];
+    Sums sums[NT / 32];
+    int warp_count[NT / 32];
     int count;
     float tau;
 };
 
 // The kk largest words of a part by kk rounds over it.  Only for parts whose
 // list is too long for another reason than ties, or short of kk because of NaN.
-template <typename T>
-MW4_DEV uint64_t top_by_rounds(const Part<T>& p, int kk, LpShared& sh) {
+template <typename T, int NT>
+MW4_DEV uint64_t top_by_rounds(const Part<T, NT>& p, int kk, LpShared<NT>& sh) {
     constexpr int E = Logit<T>::E;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     uint64_t last = ~0ull, mine = 0;
@@ -238,7 +236,7 @@ MW4_DEV uint64_t top_by_rounds(const Part<T>& p, int kk, LpShared& sh) {
             if (w < last && w > best) best = w;
         };
         if (p.scalar >= 0) see(Logit<T>::one(p.row + p.scalar), p.scalar);
-        for (int v = p.v0 + tid; v < p.v1; v += kLpThreads) {
+        for (int v = p.v0 + tid; v < p.v1; v += NT) {
             float2 x[E / 2];
             Logit<T>::split(*p.vec(v), x);
             for (int j = 0; j < E / 2; ++j) {
@@ -254,7 +252,7 @@ MW4_DEV uint64_t top_by_rounds(const Part<T>& p, int kk, LpShared& sh) {
         __syncthreads();
         if (lane == 0) sh.sorted[warp][0] = best;
         __syncthreads();
-        for (int w = 0; w < kLpWarps; ++w) best = sh.sorted[w][0] > best ? sh.sorted[w][0] : best;
+        for (int w = 0; w < (NT / 32); ++w) best = sh.sorted[w][0] > best ? sh.sorted[w][0] : best;
         if (lane == k) mine = best;
         last = best;
     }
@@ -263,8 +261,8 @@ MW4_DEV uint64_t top_by_rounds(const Part<T>& p, int kk, LpShared& sh) {
 
 // Lists the logits of the part that are >= tau (> tau where strict).  The warp
 // reads the vectors of one thread after the other that has such a logit.
-template <typename T>
-MW4_DEV void list_from(const Part<T>& p, float thread_max, float scalar, float tau, bool strict, LpShared& sh) {
+template <typename T, int NT>
+MW4_DEV void list_from(const Part<T, NT>& p, float thread_max, float scalar, float tau, bool strict, LpShared<NT>& sh) {
     constexpr int E = Logit<T>::E;
     const int lane = threadIdx.x & 31;
     auto see = [&](float x, int i) {
@@ -276,7 +274,7 @@ MW4_DEV void list_from(const Part<T>& p, float thread_max, float scalar, float t
     if (p.scalar >= 0) see(scalar, p.scalar);
     for (uint32_t hits = __ballot_sync(0xffffffffu, strict ? thread_max > tau : thread_max >= tau); hits; hits &= hits - 1) {
         const int owner = (int)(threadIdx.x & ~31u) + __ffs(hits) - 1;
-        for (int v = p.v0 + owner + lane * kLpThreads; v < p.v1; v += 32 * kLpThreads) {
+        for (int v = p.v0 + owner + lane * NT; v < p.v1; v += 32 * NT) {
             float2 x[E / 2];
             Logit<T>::split(*p.vec(v), x);
             if (max_of(x) >= tau) {
@@ -292,15 +290,15 @@ MW4_DEV void list_from(const Part<T>& p, float thread_max, float scalar, float t
 
 // Adds to the list the `need` lowest-indexed logits of the body that equal tau
 // (fewer if there are not so many), and all such logits outside it (at most 14).
-template <typename T>
-MW4_DEV void list_ties(const Part<T>& p, float tau, int need, LpShared& sh) {
+template <typename T, int NT>
+MW4_DEV void list_ties(const Part<T, NT>& p, float tau, int need, LpShared<NT>& sh) {
     constexpr int E = Logit<T>::E;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     if (p.scalar >= 0) {
         const float x = Logit<T>::one(p.row + p.scalar);
         if (x == tau) sh.list[atomicAdd(&sh.count, 1)] = logit_word(x, p.scalar);
     }
-    for (int base = p.v0; base < p.v1 && need > 0; base += kLpThreads) {
+    for (int base = p.v0; base < p.v1 && need > 0; base += NT) {
         const int v = base + tid;
         float2 x[E / 2];
         uint32_t eq = 0;
@@ -320,7 +318,7 @@ MW4_DEV void list_ties(const Part<T>& p, float tau, int need, LpShared& sh) {
         if (lane == 31) sh.warp_count[warp] = incl;
         __syncthreads();
         int before = incl - mine, all = 0;
-        for (int w = 0; w < kLpWarps; ++w) {
+        for (int w = 0; w < (NT / 32); ++w) {
             before += w < warp ? sh.warp_count[w] : 0;
             all += sh.warp_count[w];
         }
@@ -331,13 +329,13 @@ MW4_DEV void list_ties(const Part<T>& p, float tau, int need, LpShared& sh) {
 }
 
 // The kk largest words of a part, in lanes 0.. of warp 0.
-template <typename T>
-MW4_DEV uint64_t part_top(const Part<T>& p, float thread_max, float scalar, int kk, LpShared& sh) {
+template <typename T, int NT>
+MW4_DEV uint64_t part_top(const Part<T, NT>& p, float thread_max, float scalar, int kk, LpShared<NT>& sh) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     sh.lane_max[warp][lane] = warp_sort(thread_max);
     if (tid == 0) sh.count = 0;
 #pragma unroll
-    for (int half = kLpWarps / 2; half; half >>= 1) {
+    for (int half = NT / 64; half; half >>= 1) {
         __syncthreads();
         if (warp < half) {
             const float v = warp_merge(sh.lane_max[warp][lane], sh.lane_max[warp + half][lane]);
@@ -365,10 +363,10 @@ MW4_DEV uint64_t part_top(const Part<T>& p, float thread_max, float scalar, int 
         }
     }
     if (c > kLpList || c < kk) return top_by_rounds(p, kk, sh);
-    const int lists = min(kLpWarps, (c + 31) / 32);
+    const int lists = min((NT / 32), (c + 31) / 32);
     uint64_t best = 0;
     if (warp < lists) {
-        for (int at = warp * 32; at < c; at += kLpThreads) {
+        for (int at = warp * 32; at < c; at += NT) {
             const uint64_t s = warp_sort(at + lane < c ? sh.list[at + lane] : 0ull);
             best = at == warp * 32 ? s : warp_merge(best, s);
         }
@@ -382,10 +380,10 @@ MW4_DEV uint64_t part_top(const Part<T>& p, float thread_max, float scalar, int 
     return lane < kk ? best : 0ull;
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kLpThreads, kLpCtas) token_logprobs_kernel(const LogprobArgs a) {
+template <typename T, int NT>
+__global__ void __launch_bounds__(NT, kLpPerSm / NT) token_logprobs_kernel(const LogprobArgs a) {
     extern __shared__ __align__(16) uint4 ring[];
-    __shared__ LpShared sh;
+    __shared__ LpShared<NT> sh;
     constexpr int E = Logit<T>::E;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int rank = (int)cluster_rank(), ctas = (int)cluster_size();
@@ -397,7 +395,7 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas) token_logprobs_kernel(con
     const uint4* from = nullptr;
     auto load_part = [&]() {
         if (load_row < a.n) {
-            const Part<T> p(a, load_row, rank, ctas);
+            const Part<T, NT> p(a, load_row, rank, ctas);
             from = p.vec(p.v0 + tid);
             left = p.v1 - p.v0 - tid;   // of the part, from this thread's on
         }
@@ -405,12 +403,12 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas) token_logprobs_kernel(con
     load_part();
     auto load = [&](int stage) {
         if (load_row < a.n) {
-            uint4* to = &ring[stage * kLpChunk + tid];
+            uint4* to = &ring[stage * (NT * kLpVecs) + tid];
 #pragma unroll
             for (int i = 0; i < kLpVecs; ++i)
-                if (left > i * kLpThreads) cp_async_16(to + i * kLpThreads, from + i * kLpThreads);
-            from += kLpChunk;
-            left -= kLpChunk;
+                if (left > i * NT) cp_async_16(to + i * NT, from + i * NT);
+            from += (NT * kLpVecs);
+            left -= (NT * kLpVecs);
             if (left + tid <= 0) {   // the part is done: on to the next row's
                 load_row += step;
                 load_part();
@@ -423,7 +421,7 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas) token_logprobs_kernel(con
 
     int stage = 0, turn = 0;
     for (int r = first; r < a.n; r += step, turn ^= 1) {
-        const Part<T> p(a, r, rank, ctas);
+        const Part<T, NT> p(a, r, rank, ctas);
         float scalar = -INFINITY;
         if (p.scalar >= 0) scalar = Logit<T>::one(p.row + p.scalar);
         // what the end of the row needs from memory, asked for now
@@ -436,15 +434,15 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas) token_logprobs_kernel(con
         Sums s{-INFINITY, 0.f, 0.f};
         float most = -INFINITY, limit = -INFINITY;
         float2 Z = make_float2(0.f, 0.f), U = Z, minus = Z;
-        for (int rest = p.v1 - p.v0 - tid, chunks = p.chunks(); chunks; --chunks, rest -= kLpChunk) {
+        for (int rest = p.v1 - p.v0 - tid, chunks = p.chunks(); chunks; --chunks, rest -= (NT * kLpVecs)) {
             cp_async_wait<kLpStages - 2>();
             load(stage == 0 ? kLpStages - 1 : stage - 1);
-            const uint4* at = &ring[stage * kLpChunk + tid];
+            const uint4* at = &ring[stage * (NT * kLpVecs) + tid];
 #pragma unroll
             for (int i = 0; i < kLpVecs; ++i) {
-                if (rest <= i * kLpThreads) break;
+                if (rest <= i * NT) break;
                 float2 x[E / 2];
-                Logit<T>::split(at[i * kLpThreads], x);
+                Logit<T>::split(at[i * NT], x);
                 const float vm = max_of(x);
                 most = fmaxf(most, vm);
                 // The reference follows the maximum when that has outgrown it by more than
@@ -487,7 +485,7 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas) token_logprobs_kernel(con
         if (kk) word = part_top(p, most, scalar, kk, sh);
         else __syncthreads();
         if (warp == 0) {
-            s = warp_join(lane < kLpWarps ? sh.sums[lane] : Sums{-INFINITY, 0.f, 0.f});
+            s = warp_join(lane < (NT / 32) ? sh.sums[lane] : Sums{-INFINITY, 0.f, 0.f});
             if (ctas > 1) {
                 st_cluster(at_rank0(&sh.part_words[turn][rank][lane]), word);
                 if (lane < 3) st_cluster(at_rank0(&sh.part_sums[turn][rank][lane]), lane == 0 ? s.m : lane == 1 ? s.Z : s.U);
@@ -522,25 +520,12 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas) token_logprobs_kernel(con
     }
 }
 
-// CTAs of a row: as many (up to 8) as keep every SM's places filled at most once
-// and leave each CTA a stage's worth of vectors or more.
-static int row_ctas(int n, int64_t vecs, int places) {
-    int c = 1;
-    while (c < kLpMaxCluster && (int64_t)n * c * 2 <= places && vecs >= (int64_t)kLpChunk / 2 * c * 2) c *= 2;
-    return c;
-}
-
-template <typename T>
-static cudaError_t launch_logprobs(const LogprobArgs& a, cudaStream_t st) {
-    int dev = 0;
-    const int sms = sm_count(&dev);
-    if (sms < 1) return cudaErrorInvalidDevice;
+template <typename T, int NT>
+static cudaError_t launch_logprobs(const LogprobArgs& a, int ctas, int clusters, int dev, cudaStream_t st) {
+    constexpr int smem = kLpStages * kLpVecs * NT * 16;
     static std::atomic<unsigned> ready;
-    cudaError_t e = allow_smem((const void*)token_logprobs_kernel<T>, kLpSmem, ready, dev);
+    const cudaError_t e = allow_smem((const void*)token_logprobs_kernel<T, NT>, smem, ready, dev);
     if (e != cudaSuccess) return e;
-    const int places = sms * kLpCtas;
-    const int ctas = row_ctas(a.n, a.vocab / Logit<T>::E, places);
-    const int clusters = a.n < places / ctas ? a.n : places / ctas;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = ctas;
@@ -549,12 +534,31 @@ static cudaError_t launch_logprobs(const LogprobArgs& a, cudaStream_t st) {
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)(clusters * ctas));
-    cfg.blockDim = dim3(kLpThreads);
-    cfg.dynamicSmemBytes = kLpSmem;
+    cfg.blockDim = dim3(NT);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, token_logprobs_kernel<T>, a);
+    return cudaLaunchKernelEx(&cfg, token_logprobs_kernel<T, NT>, a);
+}
+
+// Few rows: CTAs of 256 threads, as many (up to 8) to a row as fit on the SMs at
+// once and still have a vector for every thread.  More rows than that: CTAs of
+// 128 threads with a row each, whose row ends are shorter and overlap better
+// (4096 x 49999 fp16: 82 us against 90; 16 x 131072 bf16: 12.0 against 10.3).
+template <typename T>
+static cudaError_t launch_logprobs(const LogprobArgs& a, cudaStream_t st) {
+    int dev = 0;
+    const int sms = sm_count(&dev);
+    if (sms < 1) return cudaErrorInvalidDevice;
+    const int places = sms * (kLpPerSm / 256), vecs = a.vocab / Logit<T>::E;
+    if (a.n > places) {
+        const int most = sms * (kLpPerSm / 128);
+        return launch_logprobs<T, 128>(a, 1, a.n < most ? a.n : most, dev, st);
+    }
+    int ctas = 1;
+    while (ctas < kLpMaxCluster && a.n * ctas * 2 <= places && vecs >= 256 * ctas * 2) ctas *= 2;
+    return launch_logprobs<T, 256>(a, ctas, a.n, dev, st);
 }
 
 }  // namespace mw4
