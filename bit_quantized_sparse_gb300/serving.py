@@ -33,8 +33,13 @@ def _need(ok, what):
         raise ValueError(what)
 
 
-def _handle(stream):
-    return (torch.cuda.current_stream() if stream is None else stream).cuda_stream
+# The current stream's handle without the Stream object around it, where torch offers that (a call saves 3 us).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _handle(stream, device):
+    return _raw_stream(device.index) if stream is None else stream.cuda_stream
 
 
 def _empty(stream, shape, dtype, device):
@@ -47,7 +52,7 @@ def _empty(stream, shape, dtype, device):
 def _new_workspace(nbytes, device, stream):
     """`nbytes` of device memory of the call's stream, cleared there."""
     ws = _empty(stream, (nbytes,), torch.uint8, device)
-    mw._check(mw.moe_w4_workspace_init(ws.data_ptr(), nbytes, _handle(stream)), "workspace_init")
+    mw._check(mw.moe_w4_workspace_init(ws.data_ptr(), nbytes, _handle(stream, device)), "workspace_init")
     return ws
 
 
@@ -136,35 +141,42 @@ class PagedKVCache:
     def _check_like_weight(self, t, dtype):
         """An array beside the cache has the layout of the cache's own weights."""
         w = self.weight
-        _need(t.dtype == dtype and t.shape == w.shape and t.device == self.device
-              and all(_stride(t, d) == _stride(w, d) for d in range(3)),
-              "expected %s with the shape and strides of the cache's weights" % dtype)
+        if not (t.dtype is dtype and t.shape == w.shape and t.device == self.device
+                and (t.stride() == w.stride() or all(_stride(t, d) == _stride(w, d) for d in range(3)))):
+            raise ValueError("expected %s with the shape and strides of the cache's weights" % dtype)
 
     def _workspace(self, nbytes, stream, handle):
+        """(address, bytes) of the stream's workspace."""
         ws = self._ws.get(handle)
-        if ws is None or ws.numel() < nbytes:
-            ws = self._ws[handle] = _new_workspace(nbytes, self.device, stream)
+        if ws is None or ws[1] < nbytes:
+            t = _new_workspace(nbytes, self.device, stream)
+            ws = self._ws[handle] = (t.data_ptr(), nbytes, t)
         return ws
-
-    def _size(self, key, ask):
-        """Workspace bytes for the sizes `key`, asked of the library once."""
-        n = self._sizes.get(key)
-        if n is None:
-            n = self._sizes[key] = max(ask(), mw.CTRL_BYTES)
-        return n
 
     def status(self) -> int:
         """The device status of the calls on this cache, all streams together (synchronises)."""
         torch.cuda.synchronize(self.device)
         got = 0
         for ws in self._ws.values():
-            got |= _word(ws)
+            got |= _word(ws[2])
         return got
 
 
+def _like(t, dtype, shape, device):
+    return t.dtype is dtype and t.shape == shape and t.device == device
+
+
 def _check_index(t, n, device, what):
-    _need(t.dtype == torch.int32 and t.dim() == 1 and t.shape[0] == n and _stride(t, 0) in (0, 1)
-          and t.device == device, what)
+    if not (_like(t, torch.int32, (n,), device) and (n <= 1 or t.stride(0) == 1)):
+        raise ValueError(what + ": contiguous int32 of %d entries on %s" % (n, device))
+
+
+def _token_stride(t, heads, dim):
+    """Elements between tokens of a [tokens][heads][dim] view, or -1 if a token is not contiguous."""
+    token, head, one = t.stride()
+    if one != 1 or (head != dim and heads > 1):
+        return -1
+    return token if t.shape[0] > 1 else 0
 
 
 def kv_append(cache: PagedKVCache, k, v, seq=None, slot=None, pos=None, stream=None) -> None:
@@ -175,20 +187,25 @@ def kv_append(cache: PagedKVCache, k, v, seq=None, slot=None, pos=None, stream=N
     pos        int32 [tokens]: position noted for eviction (None: the index); a cache with weights notes it and
                starts the token's weight at 0
     """
-    n = k.shape[0]
-    shape = (n, cache.n_kv_heads, cache.head_dim)
-    for t in (k, v):
-        _need(t.dtype == cache.dtype and t.shape == shape and t.device == cache.device and t.stride(2) == 1
-              and _stride(t, 1) in (0, cache.head_dim),
-              "k and v: [tokens][kv heads][head dim] of the cache's type, each token contiguous")
-    for t in (seq, slot, pos):
-        if t is not None:
-            _check_index(t, n, cache.device, "seq, slot and pos: contiguous int32 [tokens] on the cache's GPU")
-    h = _handle(stream)
-    ws = cache._workspace(mw.CTRL_BYTES, stream, h)
-    mw._check(mw.moe_w4_kv_append(cache._c, cache._t, n, k.data_ptr(), _stride(k, 0), v.data_ptr(), _stride(v, 0),
-                                  mw._ptr(seq), mw._ptr(slot), mw._ptr(pos), ws.data_ptr(), ws.numel(), h),
-              "moe_w4_kv_append")
+    device, heads, dim, n = cache.device, cache.n_kv_heads, cache.head_dim, k.shape[0]
+    shape = (n, heads, dim)
+    if not (_like(k, cache.dtype, shape, device) and _like(v, cache.dtype, shape, device)):
+        raise ValueError("k and v: [tokens][kv heads][head dim] of the cache's type on its GPU")
+    k_stride, v_stride = _token_stride(k, heads, dim), _token_stride(v, heads, dim)
+    if k_stride < 0 or v_stride < 0:
+        raise ValueError("k and v: each token contiguous")
+    if seq is not None:
+        _check_index(seq, n, device, "seq")
+    if slot is not None:
+        _check_index(slot, n, device, "slot")
+    if pos is not None:
+        _check_index(pos, n, device, "pos")
+    handle = _handle(stream, device)
+    ws = cache._workspace(mw.CTRL_BYTES, stream, handle)
+    status = mw.moe_w4_kv_append(cache._c, cache._t, n, k.data_ptr(), k_stride, v.data_ptr(), v_stride, mw._ptr(seq),
+                                 mw._ptr(slot), mw._ptr(pos), ws[0], ws[1], handle)
+    if status:
+        mw._check(status, "moe_w4_kv_append")
 
 
 def attend_decode(cache: PagedKVCache, q, scale: Optional[float] = None, max_len: Optional[int] = None, out=None,
@@ -202,32 +219,40 @@ def attend_decode(cache: PagedKVCache, q, scale: Optional[float] = None, max_len
                 probability that each token drew, summed over the kv head's query heads
     Returns out, or (out, lse).
     """
-    n_seqs, dim = cache.n_seqs, cache.head_dim
-    _need(q.dim() == 3 and q.dtype == cache.dtype and q.device == cache.device and q.shape[0] == n_seqs
-          and q.shape[2] == dim, "q: [sequences][query heads][head dim] of the cache's type")
-    heads = q.shape[1]
-    _need(q.stride(2) == 1 and _stride(q, 1) in (0, dim), "q: contiguous heads")
+    device, dim, dtype = cache.device, cache.head_dim, cache.dtype
+    shape = q.shape
+    if not (len(shape) == 3 and shape[0] == cache.n_seqs and shape[2] == dim and q.dtype is dtype and q.device == device):
+        raise ValueError("q: [sequences][query heads][head dim] of the cache's type on its GPU")
+    heads = shape[1]
+    q_stride = _token_stride(q, heads, dim)
     if out is None:
-        out = _empty(stream, (n_seqs, heads, dim), q.dtype, cache.device)
+        out = _empty(stream, shape, dtype, device)
+        out_stride = heads * dim
     else:
-        _need(out.shape == q.shape and out.dtype == q.dtype and out.device == q.device and out.stride(2) == 1
-              and _stride(out, 1) in (0, dim), "out: like q, contiguous heads")
-    lse = _empty(stream, (n_seqs, heads), torch.float32, cache.device) if return_lse else None
+        if not _like(out, dtype, shape, device):
+            raise ValueError("out: like q")
+        out_stride = _token_stride(out, heads, dim)
+    if q_stride < 0 or out_stride < 0:
+        raise ValueError("q and out: contiguous heads")
+    lse = _empty(stream, (shape[0], heads), torch.float32, device) if return_lse else None
     max_len = cache.capacity if max_len is None else int(max_len)
     track = None
     if weight_out is not None:
         _need(cache.weight is not None, "weight_out needs a cache with weights")
         cache._check_like_weight(weight_out, torch.float32)
         track = cache._t
-    tracked = track is not None
-    h = _handle(stream)
-    size = cache._size(("attend", heads, max_len, tracked),
-                       lambda: mw.moe_w4_attend_workspace_size(cache._c, heads, max_len, tracked))
-    ws = cache._workspace(size, stream, h)
-    mw._check(mw.moe_w4_attend_decode(cache._c, heads, q.data_ptr(), _stride(q, 0),
-                                      dim ** -0.5 if scale is None else scale, max_len, out.data_ptr(), _stride(out, 0),
-                                      mw._ptr(lse), track, mw._ptr(weight_out), ws.data_ptr(), ws.numel(), h),
-              "moe_w4_attend_decode")
+    handle = _handle(stream, device)
+    key = (heads, max_len, weight_out is not None)
+    size = cache._sizes.get(key)
+    if size is None:
+        size = max(mw.moe_w4_attend_workspace_size(cache._c, heads, max_len, key[2]), mw.CTRL_BYTES)
+        cache._sizes[key] = size
+    ws = cache._workspace(size, stream, handle)
+    status = mw.moe_w4_attend_decode(cache._c, heads, q.data_ptr(), q_stride, dim ** -0.5 if scale is None else scale,
+                                     max_len, out.data_ptr(), out_stride, mw._ptr(lse), track, mw._ptr(weight_out),
+                                     ws[0], ws[1], handle)
+    if status:
+        mw._check(status, "moe_w4_attend_decode")
     return (out, lse) if return_lse else out
 
 
@@ -238,11 +263,12 @@ def kv_evict(cache: PagedKVCache, seen, budget: int, sink: int = 0, recent: int 
     accumulated weight.  Keys and values move inside the cache; lengths, weights and positions go to lens_out,
     weight_out and pos_out (default: cache.seq_lens, cache.weight and cache.pos, in place)."""
     _need(cache.pos is not None, "eviction needs a cache with weights and positions")
-    _check_index(seen, cache.n_seqs, cache.device, "seen: contiguous int32 [sequences] on the cache's GPU")
+    device = cache.device
+    _check_index(seen, cache.n_seqs, device, "seen")
     if lens_out is None:
         lens_out = cache.seq_lens
     else:
-        _check_index(lens_out, cache.n_seqs, cache.device, "lens_out: contiguous int32 [sequences] on the cache's GPU")
+        _check_index(lens_out, cache.n_seqs, device, "lens_out")
     if weight_out is None:
         weight_out = cache.weight
     else:
@@ -252,13 +278,16 @@ def kv_evict(cache: PagedKVCache, seen, budget: int, sink: int = 0, recent: int 
     else:
         cache._check_like_weight(pos_out, torch.int32)
     max_len = min(cache.capacity, cache.weight.shape[2]) if max_len is None else int(max_len)
-    budget = int(budget)
-    h = _handle(stream)
-    size = cache._size(("evict", budget, max_len), lambda: mw.moe_w4_evict_workspace_size(cache._c, budget, max_len))
-    ws = cache._workspace(size, stream, h)
-    mw._check(mw.moe_w4_kv_evict(cache._c, cache._t, seen.data_ptr(), budget, sink, recent, max_len,
-                                 lens_out.data_ptr(), weight_out.data_ptr(), pos_out.data_ptr(), ws.data_ptr(),
-                                 ws.numel(), h), "moe_w4_kv_evict")
+    handle = _handle(stream, device)
+    key = (int(budget), max_len)
+    size = cache._sizes.get(key)
+    if size is None:
+        size = cache._sizes[key] = max(mw.moe_w4_evict_workspace_size(cache._c, *key), mw.CTRL_BYTES)
+    ws = cache._workspace(size, stream, handle)
+    status = mw.moe_w4_kv_evict(cache._c, cache._t, seen.data_ptr(), key[0], sink, recent, max_len, lens_out.data_ptr(),
+                                weight_out.data_ptr(), pos_out.data_ptr(), ws[0], ws[1], handle)
+    if status:
+        mw._check(status, "moe_w4_kv_evict")
 
 
 class TokenLogprobs(NamedTuple):
@@ -268,7 +297,7 @@ class TokenLogprobs(NamedTuple):
     top_logprob: Optional[torch.Tensor]   # fp32 [rows][top]
 
 
-_ctrl = {}   # (device, stream) -> control header of the log-probability calls there
+_ctrl = {}   # (device index, stream) -> control header of the log-probability calls there, and its address
 
 
 def token_logprobs(logits, targets=None, top: int = 0, stream=None) -> TokenLogprobs:
@@ -276,25 +305,35 @@ def token_logprobs(logits, targets=None, top: int = 0, stream=None) -> TokenLogp
     (natural logarithms), and the `top` most likely tokens, best first, the lower index first among equals.
 
     logits: fp32, bf16 or fp16 [rows][vocabulary], contiguous rows."""
-    _need(logits.dim() == 2 and logits.dtype in _TYPES and logits.is_cuda, "logits: a 2-D tensor on the GPU")
+    kind = _TYPES.get(logits.dtype)
+    if kind is None or logits.dim() != 2 or not logits.is_cuda:
+        raise ValueError("logits: a 2-D fp32, bf16 or fp16 tensor on the GPU")
     n, vocab = logits.shape
-    _need(_stride(logits, 1) in (0, 1), "logits: contiguous rows")
-    dev = logits.device
+    row, one = logits.stride()
+    if one != 1 and vocab > 1:
+        raise ValueError("logits: contiguous rows")
+    device = logits.device
     if targets is not None:
-        _check_index(targets, n, dev, "targets: contiguous int32 [rows] on the logits' GPU")
-    h = _handle(stream)
-    ws = _ctrl.get((dev, h))
+        _check_index(targets, n, device, "targets")
+    handle = _handle(stream, device)
+    key = (device.index, handle)
+    ws = _ctrl.get(key)
     if ws is None:
-        ws = _ctrl[dev, h] = _new_workspace(mw.CTRL_BYTES, dev, stream)
-    logprob = None if targets is None else _empty(stream, (n,), torch.float32, dev)
-    entropy = _empty(stream, (n,), torch.float32, dev)
-    index = value = None
+        t = _new_workspace(mw.CTRL_BYTES, device, stream)
+        ws = _ctrl[key] = (t.data_ptr(), t)
+    logprob = index = value = None
+    if targets is None:
+        entropy = _empty(stream, (n,), torch.float32, device)
+    else:
+        entropy, logprob = _empty(stream, (2, n), torch.float32, device).unbind()
     if top:
-        index = _empty(stream, (n, top), torch.int32, dev)
-        value = _empty(stream, (n, top), torch.float32, dev)
-    mw._check(mw.moe_w4_token_logprobs(_TYPES[logits.dtype], n, vocab, logits.data_ptr(), _stride(logits, 0),
-                                       mw._ptr(targets), top, mw._ptr(logprob), entropy.data_ptr(), mw._ptr(index),
-                                       mw._ptr(value), ws.data_ptr(), mw.CTRL_BYTES, h), "moe_w4_token_logprobs")
+        index = _empty(stream, (n, top), torch.int32, device)
+        value = _empty(stream, (n, top), torch.float32, device)
+    status = mw.moe_w4_token_logprobs(kind, n, vocab, logits.data_ptr(), row if n > 1 else 0, mw._ptr(targets), top,
+                                      mw._ptr(logprob), entropy.data_ptr(), mw._ptr(index), mw._ptr(value), ws[0],
+                                      mw.CTRL_BYTES, handle)
+    if status:
+        mw._check(status, "moe_w4_token_logprobs")
     return TokenLogprobs(logprob, entropy, index, value)
 
 
@@ -303,5 +342,5 @@ def logprobs_status() -> int:
     torch.cuda.synchronize()
     got = 0
     for ws in _ctrl.values():
-        got |= _word(ws)
+        got |= _word(ws[1])
     return got
