@@ -322,10 +322,9 @@ def token_logprobs(logits, targets=None, top: int = 0, stream=None) -> TokenLogp
         t = _new_workspace(mw.CTRL_BYTES, device, stream)
         ws = _ctrl[key] = (t.data_ptr(), t)
     logprob = index = value = None
-    if targets is None:
-        entropy = _empty(stream, (n,), torch.float32, device)
-    else:
-        entropy, logprob = _empty(stream, (2, n), torch.float32, device).unbind()
+    entropy = _empty(stream, (n,), torch.float32, device)
+    if targets is not None:
+        logprob = _empty(stream, (n,), torch.float32, device)
     if top:
         index = _empty(stream, (n, top), torch.int32, device)
         value = _empty(stream, (n, top), torch.float32, device)
