@@ -6,18 +6,30 @@
 // Each token's keys and values are read once for the `group` query heads that
 // share them: 4 D bytes per token and kv head for 4 D group flops, so HBM
 // bounds it, and only the tensor pipe keeps the products out of the way (fp32
-// FMAs would already bound it at a group of 8).
+// FMAs would already bound it at a group of 8).  mma.sync is enough here: a
+// tcgen05 tile of 128 rows would be nearly empty at 1 to 16 query heads.
 //
 // Work split.  A row is a (sequence, kv head, block of up to 16 query heads);
 // its tokens are cut into tiles of 64.  The tiles of all rows, in order, form
 // one list that the CTAs of a resident grid share out in equal contiguous
 // parts, so mixed lengths balance without the host knowing them.  A row that
 // crosses CTAs leaves partial results (running maximum, sum, unnormalised
-// output) that attend_join_kernel adds up in CTA order.
+// output); at the end each of its CTAs waits for all of them (a cooperative
+// launch, bounded waits) and adds up its own share of the row's output in CTA
+// order, so that the join is spread over the CTAs too.
 //
 // Each warp is a pipeline of its own: it owns 16 tokens of every tile, keeps
-// them arriving through cp.async several tiles ahead (across row ends), and
-// holds its own running maximum, sum and output; warps meet only at row ends.
+// their keys and values arriving through cp.async in a ring of its own (units
+// of 16 rows, across row ends), and holds its own running maximum, sum and
+// output; warps meet only at row ends.
+//
+// Products are taken transposed, tokens (keys) or dimensions (values) as the 16
+// rows of an MMA and 8 query heads as its columns: S^T = K q^T, O^T = V^T P^T.
+// With queries as rows instead half of every product was empty at a group of
+// 8; 870 instructions per 16 tokens of 256 dimensions became about 300, and
+// issue latency, not HBM, had been the limit (131,072 tokens: 51 us).
+#include <climits>
+
 #include "serving.cuh"
 
 namespace mw4 {
@@ -27,15 +39,24 @@ constexpr int kAttThreads = kAttWarps * 32;
 constexpr int kSub = 16;                        // tokens of a warp's part of a tile
 constexpr int kTile = kSub * kAttWarps;
 constexpr int kHeads = 16;                      // query heads of a row, at most
-constexpr int kMaxCtas = 152 * 3;               // partial records the workspace has room for
+constexpr int kMaxSms = 160;                    // SMs that the workspace has room for
 constexpr float kLazyRescale = 8.f;             // log2 growth of the maximum before a rescale
 
-// Pipeline depth and CTAs per SM for a head size: about 100 to 200 KB of shared
-// memory of every SM holds tiles in flight.
+// Ring units per warp and CTAs per SM for a head size: about 190 KB of every SM
+// hold units in flight.
 template <int D> struct AttCfg;
-template <> struct AttCfg<64> { static constexpr int stages = 4, ctas = 3; };
-template <> struct AttCfg<128> { static constexpr int stages = 3, ctas = 2; };
-template <> struct AttCfg<256> { static constexpr int stages = 3, ctas = 1; };
+template <> struct AttCfg<64> { static constexpr int slots = 5, ctas = 4; };
+template <> struct AttCfg<128> { static constexpr int slots = 3, ctas = 3; };
+template <> struct AttCfg<256> { static constexpr int slots = 2, ctas = 2; };
+constexpr int unit_bytes(int dim) { return kSub * dim * 2 + 128; }   // 128 more for the pitch of a warp's outputs
+constexpr int most_ctas(int dim) { return kMaxSms * (dim == 64 ? AttCfg<64>::ctas : dim == 128 ? AttCfg<128>::ctas : AttCfg<256>::ctas); }
+
+// Arrivals at a split row, by the first of its CTAs: how many partial results
+// are there, and how many of the row's CTAs are done with them.  The last to
+// leave clears both, so a finished call leaves zeros.
+struct RowSync {
+    unsigned int arrived, left;
+};
 
 struct AttendArgs {
     KvView c;
@@ -43,17 +64,22 @@ struct AttendArgs {
     uint16_t* out;
     float* lse;         // or NULL
     int64_t q_stride, out_stride;
+    const uint4* k;     // the pools and their strides in pieces of 16 bytes
+    const uint4* v;
+    uint32_t page_pieces, head_pieces, slot_pieces;
     int n_q_heads, group, head_blocks, max_len;
+    int runs;           // pages of a multiple of 16 slots: 16 tokens are one run in memory
     float scale_log2;   // scale * log2(e)
     float* part_o;      // [2 * CTAs][kHeads][D] unnormalised outputs
     float* part_ml;     // [2 * CTAs][kHeads][2] running maximum (log2) and sum
+    RowSync* sync;      // [CTAs]
     float* scores;      // [n_seqs][n_q_heads][score_stride] log2 scores, or NULL
     float* lse2;        // [n_seqs][n_q_heads] log2 of the sums, with scores
     int64_t score_stride;
     const float* weight;
     float* weight_out;
     int64_t track_seq, track_head;
-    unsigned int* status;
+    Ctrl* ctrl;
 };
 
 template <typename T> struct Elem;
@@ -90,52 +116,76 @@ MW4_DEV void ldsm4_t(uint32_t (&r)[4], uint32_t addr) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
 }
+// An 8 x 8 block of 16-bit values, two a lane, transposed.
+MW4_DEV uint32_t transpose8(uint32_t v) {
+    uint32_t d;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(v));
+    return d;
+}
+MW4_DEV void cp_async_16_to(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" :: "r"(dst), "l"(src) : "memory");
+}
 // 16 bytes, or zeros where !there (the source is not read then).
 MW4_DEV void cp_async_16_or_zero(uint32_t dst, const void* src, bool there) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" :: "r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
 }
+MW4_DEV unsigned int ld_acquire(const unsigned int* p) {
+    unsigned int v;
+    asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+    return v;
+}
 
-// The list of tiles and its shares.  total >= 1; part c of `parts` starts at
-// tile floor(c total / parts); parts <= total, so no part is empty.
+// The list and its shares: 1 <= total < 2^31 places in `parts` <= total parts of
+// q places, the first r of them one longer.
 struct Shares {
-    int64_t total;
-    int parts;
-    MW4_DEV int64_t start(int c) const { return c * total / parts; }
-    MW4_DEV int owner(int64_t tile) const { return (int)(((tile + 1) * parts - 1) / total); }
+    uint32_t total, parts, q, r;
+    MW4_DEV Shares(uint32_t places, uint32_t most) : total(places), parts(min(most, places)) {
+        q = total / parts;
+        r = total - q * parts;
+    }
+    MW4_DEV uint32_t start(uint32_t c) const { return c * q + min(c, r); }
+    MW4_DEV int owner(uint32_t place) const {
+        const uint32_t longer = r * (q + 1);
+        return (int)(place < longer ? place / (q + 1) : r + (place - longer) / q);
+    }
 };
 
 MW4_DEV int tiles_of(int len) { return max(1, (len + kTile - 1) / kTile); }
+// Places of a row in the list: its tiles and kRowCost more, with no tokens, for
+// what the end of a row costs, about the time of a tile.  Without them the CTAs
+// that got the short sequences of a mixed batch were the last by far (16
+// sequences of 1 to 32,768 tokens: 75 us).
+constexpr int kRowCost = 1;
+MW4_DEV uint32_t places_of(int len) { return tiles_of(len) + kRowCost; }
 
 MW4_DEV int checked_len(const AttendArgs& a, int b) {
     const int n = a.c.lens[b];
     return n < 0 ? 0 : min(n, a.max_len);
 }
 
-// Sum of tiles_of over the sequences [0, end); every thread of a warp gets it.
-MW4_DEV int64_t warp_tiles(const AttendArgs& a, int end) {
-    int64_t n = 0;
-    for (int b = threadIdx.x & 31; b < end; b += 32) n += tiles_of(checked_len(a, b));
-#pragma unroll
-    for (int off = 16; off; off >>= 1) n += __shfl_xor_sync(0xffffffffu, n, off);
-    return n;
+// Sum of places_of over the sequences; every thread of a warp gets it.
+MW4_DEV uint32_t warp_places(const int* lens, int n_seqs) {
+    uint32_t n = 0;
+    for (int b = threadIdx.x & 31; b < n_seqs; b += 32) n += places_of(lens[b]);
+    return __reduce_add_sync(0xffffffffu, n);
 }
 
-// The sequence that holds tile x of the list and the first tile of that
+// The sequence that holds place x of the list and the first place of that
 // sequence, found by a whole warp.
-MW4_DEV void find_seq(const AttendArgs& a, int rows, int64_t x, int& b, int64_t& first) {
+MW4_DEV void find_seq(const int* lens, int n_seqs, uint32_t rows, uint32_t x, int& b, uint32_t& first) {
     const int lane = threadIdx.x & 31;
-    int64_t base = 0;
+    uint32_t base = 0;
     for (int b0 = 0;; b0 += 32) {
-        const int mine = b0 + lane < a.c.n_seqs ? tiles_of(checked_len(a, b0 + lane)) : 0;
-        int64_t incl = mine;
+        const uint32_t mine = b0 + lane < n_seqs ? places_of(lens[b0 + lane]) : 0;
+        uint32_t incl = mine;
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
-            const int64_t o = __shfl_up_sync(0xffffffffu, incl, off);
+            const uint32_t o = __shfl_up_sync(0xffffffffu, incl, off);
             if (lane >= off) incl += o;
         }
         const uint32_t past = __ballot_sync(0xffffffffu, (base + incl) * rows > x);
-        if (past || b0 + 32 >= a.c.n_seqs) {
-            const int at = past ? __ffs(past) - 1 : 31;
+        if (past) {   // always so for x below the total, at the last sequences if not before
+            const int at = __ffs(past) - 1;
             b = b0 + at;
             first = (base + __shfl_sync(0xffffffffu, incl - mine, at)) * rows;
             return;
@@ -148,393 +198,530 @@ MW4_DEV void find_seq(const AttendArgs& a, int rows, int64_t x, int& b, int64_t&
 struct Place {
     int b, row, tile, tiles, len;
 };
-MW4_DEV void next_place(const AttendArgs& a, int rows, Place& p) {
-    if (++p.tile < p.tiles) return;
+MW4_DEV void next_row(const int* lens, int n_seqs, int rows, Place& p) {
     p.tile = 0;
     if (++p.row < rows) return;
     p.row = 0;
-    if (++p.b >= a.c.n_seqs) return;   // past the end: not used
-    p.len = checked_len(a, p.b);
+    if (++p.b >= n_seqs) return;   // past the end: not used
+    p.len = lens[p.b];
     p.tiles = tiles_of(p.len);
 }
 
-// GT: query heads of a row, 8 or 16.  The A operand of an MMA has 16 rows.
-// With 8 heads the probabilities' upper 8 rows hold what rounding to 16 bits
-// took from the lower 8, so they enter the product with about 16 (bf16) or 22
-// (fp16) bits at no extra cost; with 16 heads that takes a second product.
-template <typename T, int D, int GT>
+// lse from a head's maximum (log2) and sum; none: no token, or none with a score
+// above -inf.
+MW4_DEV void write_lse(const AttendArgs& a, int b, int head, float M, float L, bool none) {
+    const float lse2 = none ? -INFINITY : M + log2f(L);
+    const int64_t at = (int64_t)b * a.n_q_heads + head;
+    if (a.lse) a.lse[at] = lse2 * kLn2;
+    if (a.scores) a.lse2[at] = lse2;
+}
+
+// Adds up this CTA's share of the output of a row that `parts` CTAs have worked
+// on, c0 first; this is number `me` of them.  Returns false if a wait ran out.
+template <typename T, int D>
+MW4_DEV bool join_row(const AttendArgs& a, uint8_t* smem, int b, int row, int c0, int parts, int me) {
+    __shared__ int sh_ok;
+    const int tid = threadIdx.x;
+    const int kvh = row / a.head_blocks, hb = row % a.head_blocks;
+    const int heads = min(kHeads, a.group - hb * kHeads), head0 = kvh * a.group + hb * kHeads;
+    __syncthreads();   // the ring and sh_ok are free
+    if (tid == 0) {
+        bool ok = true;
+        const uint64_t t0 = globaltimer();
+        for (int it = 0; ld_acquire(&a.sync[c0].arrived) < (unsigned)parts; ++it)
+            if ((it & 15) == 15 && globaltimer() - t0 > kWaitLimitNs) {
+                raise_status(&a.ctrl->status, MOE_W4_STATUS_WAIT_TIMEOUT);
+                ok = false;
+                break;
+            }
+        sh_ok = ok;
+    }
+    __syncthreads();
+    if (!sh_ok) return false;
+    auto slot = [&](int i) { return (int64_t)((c0 + i) * 2 + (i == 0 ? 1 : 0)) * kHeads; };
+    // This CTA's columns of four outputs, and the heads that they belong to.
+    constexpr int Q = D / 4;                                  // columns of a head
+    const int total = heads * Q, per = (total + parts - 1) / parts;
+    const int lo = me * per, cols = min(per, total - lo);
+    if (cols > 0) {
+        // everything the sums need in one trip, a warp for a part in turn: the heads'
+        // maxima and sums (by pairs of heads), and the columns
+        const int h0 = lo / Q & ~1, pairs = (lo + cols - 1) / Q / 2 - h0 / 2 + 1;
+        float4* ml = reinterpret_cast<float4*>(smem);         // [parts][pairs]: m, sum, m, sum
+        float4* part = ml + parts * pairs;                    // [parts][cols]
+        const int lane = tid & 31, warp = tid >> 5;
+        // few columns: several parts to a warp
+        const int wide = max(cols, pairs), lanes = wide >= 32 ? 32 : wide > 16 ? 32 : wide > 8 ? 16 : wide > 4 ? 8 : 4;
+        const int sub = lane / lanes, in = lane & (lanes - 1), subs = 32 / lanes;
+#pragma unroll 1
+        for (int i = warp * subs + sub; i < parts; i += kAttWarps * subs) {
+            const int64_t sl = slot(i);
+            for (int e = in; e < pairs; e += lanes) cp_async_16(&ml[i * pairs + e], a.part_ml + (sl + h0 + e * 2) * 2);
+            for (int e = in; e < cols; e += lanes) cp_async_16(&part[i * cols + e], a.part_o + sl * D + (lo + e) * 4);
+        }
+        cp_async_commit();
+        cp_async_wait<0>();
+        __syncthreads();
+        // a group of lanes for a column, its lanes taking turns at the parts
+        const int turns = cols >= 128 ? 1 : cols >= 64 ? 2 : cols >= 32 ? 4 : cols >= 16 ? 8 : cols >= 8 ? 16 : 32;
+        const int turn = tid & (turns - 1);
+#pragma unroll 1
+        for (int e = tid / turns; e < cols + kAttThreads / turns; e += kAttThreads / turns) {
+            if (e - tid / turns >= cols) break;   // the same for every lane
+            const int mine = min(e, cols - 1), h = (lo + mine) / Q;
+            const float2* of = reinterpret_cast<const float2*>(ml) + h - h0;   // the head's, 2 pairs apart
+            float M = -INFINITY, L = 0.f;
+#pragma unroll 1
+            for (int i = turn; i < parts; i += turns) M = fmaxf(M, of[i * 2 * pairs].x);
+#pragma unroll 1
+            for (int off = turns / 2; off; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+            for (int i = turn; i < parts; i += turns) {
+                const float2 x = of[i * 2 * pairs];
+                const float4 p = part[i * cols + mine];
+                const float f = x.x == -INFINITY ? 0.f : ex2(x.x - M);
+                L += x.y * f;
+                v.x += p.x * f; v.y += p.y * f; v.z += p.z * f; v.w += p.w * f;
+            }
+#pragma unroll 1
+            for (int off = turns / 2; off; off >>= 1) {
+                L += __shfl_xor_sync(0xffffffffu, L, off);
+                v.x += __shfl_xor_sync(0xffffffffu, v.x, off);
+                v.y += __shfl_xor_sync(0xffffffffu, v.y, off);
+                v.z += __shfl_xor_sync(0xffffffffu, v.z, off);
+                v.w += __shfl_xor_sync(0xffffffffu, v.w, off);
+            }
+            if (e < cols && turn == 0) {
+                const bool none = M == -INFINITY && L == 0.f;
+                const float inv = none ? 0.f : 1.f / L;
+                const int col = (lo + e - h * Q) * 4;
+                *reinterpret_cast<uint2*>(a.out + b * a.out_stride + (int64_t)(head0 + h) * D + col) =
+                    make_uint2(Elem<T>::pack(v.x * inv, v.y * inv), Elem<T>::pack(v.z * inv, v.w * inv));
+                if (col == 0) write_lse(a, b, head0 + h, M, L, none);
+            }
+        }
+    }
+    if (tid == 0) {   // the last to leave clears the row's record
+        if (atomic_add_acq_rel_gpu(&a.sync[c0].left, 1) == (unsigned)parts - 1) {
+            a.sync[c0].arrived = 0;
+            a.sync[c0].left = 0;
+        }
+    }
+    return true;
+}
+
+// NB: blocks of 8 query heads of a row, 1 or 2.
+template <typename T, int D, int NB>
 __global__ void __launch_bounds__(kAttThreads, AttCfg<D>::ctas) attend_kernel(const AttendArgs a) {
     extern __shared__ __align__(1024) uint8_t smem[];
     __shared__ float sh_m[kAttWarps][kHeads], sh_l[kAttWarps][kHeads];
-    constexpr int S = AttCfg<D>::stages;
+    constexpr int S = AttCfg<D>::slots;
     constexpr int ROW = D * 2;                       // bytes of a token's keys
-    constexpr int HALF = kSub * ROW, STAGE = 2 * HALF;
+    constexpr int UNIT = unit_bytes(D);              // keys or values of 16 tokens
     constexpr int CH = D / 8;                        // 16-byte pieces of a row
+    constexpr int PER = 32 / CH, STEPS = kSub / PER; // rows of a warp-wide copy
+    constexpr int TURN = 8 / PER;                    // copies until the swizzle repeats
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int g = lane >> 2, t4 = lane & 3;
-    uint8_t* ring = smem + warp * S * STAGE;
-    const uint32_t ring_u = smem_u32(ring);
+    uint8_t* ring = smem + warp * S * UNIT;
+    const uint32_t ring_u = smem_u32(ring), ring_end = ring_u + S * UNIT;
     griddep_wait();
 
-    const int rows = a.c.n_kv_heads * a.head_blocks;
-    Shares sh;
-    sh.total = warp_tiles(a, a.c.n_seqs) * rows;
-    sh.parts = (int)min((int64_t)gridDim.x, sh.total);
-    const int cta = blockIdx.x;
+    // The lengths, read once: whatever happens to them meanwhile, this CTA's view
+    // of the list is one, and its accesses stay in range.
+    const int rows = a.c.n_kv_heads * a.head_blocks, n_seqs = a.c.n_seqs;
+    int* lens = reinterpret_cast<int*>(smem + kAttWarps * S * UNIT);
+    const uint32_t cta = blockIdx.x;
+    for (int b = threadIdx.x; b < n_seqs; b += kAttThreads) {
+        const int n = a.c.lens[b];
+        if (cta == 0 && (n < 0 || n > a.max_len)) raise_status(&a.ctrl->status, MOE_W4_STATUS_BAD_INDEX);
+        lens[b] = n < 0 ? 0 : min(n, a.max_len);
+    }
+    __syncthreads();
+    const Shares sh(warp_places(lens, n_seqs) * rows, gridDim.x);
     if (cta >= sh.parts) return;
-    const int64_t x0 = sh.start(cta);
-    const int items = (int)(sh.start(cta + 1) - x0);
-    Place ld;
-    int64_t seq_first;
-    find_seq(a, rows, x0, ld.b, seq_first);
-    ld.len = checked_len(a, ld.b);
-    ld.tiles = tiles_of(ld.len);
-    ld.row = (int)((x0 - seq_first) / ld.tiles);
-    ld.tile = (int)((x0 - seq_first) % ld.tiles);
-    Place at = ld;
-    if (cta == 0)
-        for (int b = threadIdx.x; b < a.c.n_seqs; b += kAttThreads)
-            if (a.c.lens[b] < 0 || a.c.lens[b] > a.max_len) raise_status(a.status, MOE_W4_STATUS_BAD_INDEX);
+    uint32_t place = sh.start(cta);                       // of `at` in the list
+    const uint32_t end = sh.start(cta + 1);
+    Place at;
+    uint32_t seq_first;
+    find_seq(lens, n_seqs, rows, place, at.b, seq_first);
+    at.len = lens[at.b];
+    at.tiles = tiles_of(at.len);
+    at.row = (int)((place - seq_first) / places_of(at.len));
+    at.tile = (int)(place - seq_first - at.row * places_of(at.len));
+    if (at.tile >= at.tiles) {                            // past a row's tiles: on to the next
+        place += places_of(at.len) - at.tile;
+        if (place >= end) return;
+        next_row(lens, n_seqs, rows, at);
+    }
 
-    // the row of the cache that lane & 15 looks up for the next tile to load
-    int64_t off = -1;
-    auto look_up = [&]() {
-        const int t = ld.tile * kTile + warp * kSub + (lane & 15);
-        off = -1;
-        if (t < ld.len) {
-            off = kv_offset(a.c, ld.b, t);
-            if (off < 0) raise_status(a.status, MOE_W4_STATUS_BAD_INDEX);
-            else off += (ld.row / a.head_blocks) * a.c.head_stride;
+    // ---- loads: units in order, keys and values of one tile after the other ----
+    // Offsets are in pieces of 16 bytes.  The block table is read one tile ahead of
+    // the keys: behind a full queue of them that load takes microseconds.
+    Place ld = at;                 // the tile loaded next
+    int left = (int)(end - place); // places from ld's tile on; none left: nothing more to load
+    int token = at.tile * kTile + warp * kSub + (lane & 15);   // of ld's tile, this lane's to look up
+    int page = -1;                 // of token
+    uint64_t head_off = 0;         // of ld's row
+    uint64_t off = 0;              // of ld's tile: this lane's first piece of a run, or its token's row
+    bool run = false, any = false, there = false;
+    auto read_page = [&](const Place& p, int t) {   // the page of token t of p's row
+        int v = -1;
+        if (t < p.len) {
+            const uint32_t e = div_by((uint32_t)t, a.c.page);
+            if (e < (uint32_t)a.c.pages_per_seq) v = a.c.table[p.b * a.c.table_stride + e];
         }
+        return v;
     };
-    auto load = [&](int stage) {
-        const uint32_t base = ring_u + stage * STAGE;
-        if (ld.tile * kTile + warp * kSub < ld.len) {
-            constexpr int PER = 32 / CH > 0 ? 32 / CH : 1;   // rows of one warp-wide copy
-            constexpr int STEPS = kSub / PER;
-            const int piece = lane % CH;
+    const int piece = lane % CH, row0 = lane / CH;
+    auto head_of = [&](const Place& p) { return (uint64_t)(p.row / a.head_blocks) * a.head_pieces; };
+    auto look_up = [&]() {         // `page` has arrived: where ld's tile is
+        const int t0 = token - (lane & 15);
+        const uint32_t in = (uint32_t)token - div_by((uint32_t)token, a.c.page) * a.c.page.d;
+        any = t0 < ld.len;
+        there = (unsigned)page < (unsigned)a.c.num_pages;
+        const bool bad = token < ld.len && !there;
+        run = a.runs && t0 + kSub <= ld.len;
+        if (__any_sync(0xffffffffu, bad)) {
+            if (bad) raise_status(&a.ctrl->status, MOE_W4_STATUS_BAD_INDEX);
+            run = false;
+        }
+        // of a run every lane's token is in one page; a lane starts at row row0 of it
+        const uint32_t r = run ? in - (lane & 15) + row0 : in;
+        off = head_off + (uint64_t)(uint32_t)page * a.page_pieces + (uint64_t)r * a.slot_pieces + (run ? piece : 0);
+    };
+    uint32_t swizzle[TURN];        // of this lane's piece in the rows that it copies
 #pragma unroll
+    for (int i = 0; i < TURN; ++i) swizzle[i] = row0 * ROW + ((piece ^ ((i * PER + row0) & 7)) << 4);
+    const bool packed = a.slot_pieces == CH;   // a run's rows follow one another
+    auto load = [&](uint32_t base, const uint4* pool) {
+        if (run) {
+            const uint4* p = pool + off;
+            uint32_t to[TURN];
+#pragma unroll
+            for (int i = 0; i < TURN; ++i) to[i] = base + swizzle[i];
+            if (packed) {
+#pragma unroll
+                for (int i = 0; i < STEPS; ++i) cp_async_16_to(to[i % TURN] + i * PER * ROW, p + i * PER * CH);
+            } else {
+                const uint32_t step = PER * a.slot_pieces;
+#pragma unroll
+                for (int i = 0; i < STEPS; ++i) cp_async_16_to(to[i % TURN] + i * PER * ROW, p + (uint64_t)i * step);
+            }
+        } else if (any) {
+#pragma unroll 1
             for (int i = 0; i < STEPS; ++i) {
-                const int r = i * PER + lane / CH;
-                const int64_t o = __shfl_sync(0xffffffffu, off, r);
-                const uint32_t dst = base + r * ROW + ((piece ^ (r & 7)) << 4);
-                const int64_t e = (o < 0 ? 0 : o) + piece * 8;
-                cp_async_16_or_zero(dst, a.c.k + e, o >= 0);
-                cp_async_16_or_zero(dst + HALF, a.c.v + e, o >= 0);
+                const int r = i * PER + row0;
+                const uint64_t o = __shfl_sync(0xffffffffu, off, r);
+                const bool ok = __shfl_sync(0xffffffffu, there, r);
+                cp_async_16_or_zero(base + r * ROW + ((piece ^ (r & 7)) << 4), pool + (ok ? o + piece : 0), ok);
             }
         }
         cp_async_commit();
     };
-
-    int loaded = 0;
-    look_up();
-#pragma unroll
-    for (int i = 0; i < S - 1; ++i) {
-        if (loaded < items) {
-            load(i);
-            next_place(a, rows, ld);
-            ++loaded;
-            if (loaded < items) look_up();
+    int next_page = -1;            // read ahead, of the tile after ld
+    Place ahead = at;
+    int ahead_token = token;
+    int ahead_left = left;
+    auto read_ahead = [&]() {
+        --ahead_left;
+        if (++ahead.tile == ahead.tiles) {
+            ahead_left -= kRowCost;
+            next_row(lens, n_seqs, rows, ahead);
+            ahead_token = warp * kSub + (lane & 15);
+        } else {
+            ahead_token += kTile;
+        }
+        if (ahead_left > 0) next_page = read_page(ahead, ahead_token);
+    };
+    uint32_t fill = ring_u;
+    bool values = false;           // the next unit is one of values
+    auto load_unit = [&]() {
+        if (left > 0) {
+            load(fill, values ? a.v : a.k);
+            if (values && (left = ahead_left) > 0) {
+                if (ahead.row != ld.row || ahead.b != ld.b) head_off = head_of(ahead);
+                ld = ahead;
+                token = ahead_token;
+                page = next_page;
+                look_up();
+                read_ahead();
+            }
         } else {
             cp_async_commit();
         }
+        values = !values;
+        fill = fill + UNIT == ring_end ? ring_u : fill + UNIT;
+    };
+    page = read_page(ld, token);
+    head_off = head_of(ld);
+    read_ahead();
+
+    // ---- the queries of a row, and its running results ----
+    uint32_t qf[NB][D / 16][2];
+    float o[NB][D / 16][4], m[NB][2], l[NB][2];
+    auto load_q = [&](const Place& p) {
+        const int kvh = p.row / a.head_blocks, hb = p.row % a.head_blocks;
+        const int heads = min(kHeads, a.group - hb * kHeads);
+        const uint16_t* q = a.q + p.b * a.q_stride + (int64_t)(kvh * a.group + hb * kHeads + g) * D + 2 * t4;
+#pragma unroll
+        for (int n = 0; n < NB; ++n)
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+                const bool in = g + 8 * n < heads;
+                qf[n][kk][0] = in ? *reinterpret_cast<const uint32_t*>(q + n * 8 * D + kk * 16) : 0u;
+                qf[n][kk][1] = in ? *reinterpret_cast<const uint32_t*>(q + n * 8 * D + kk * 16 + 8) : 0u;
+            }
+    };
+    load_q(at);
+    look_up();
+    // lanes' places in a unit of keys (rows tokens) and of values (rows tokens, transposed)
+    uint32_t k_lane[4], v_lane[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int kt = lane & 15, vt = (lane & 7) + ((lane >> 4) << 3);
+        k_lane[i] = kt * ROW + (((i * 2 + (lane >> 4)) ^ (kt & 7)) << 4);
+        v_lane[i] = vt * ROW + (((i * 2 + ((lane >> 3) & 1)) ^ (vt & 7)) << 4);
     }
 
-    uint32_t qf[D / 16][4];
-    float o[D / 8][4], m[2], l[2];
-    auto start_row = [&]() {
-        const int kvh = at.row / a.head_blocks, hb = at.row % a.head_blocks;
-        const int heads = min(kHeads, a.group - hb * kHeads);
-        const uint16_t* q = a.q + at.b * a.q_stride + (int64_t)(kvh * a.group + hb * kHeads) * D;
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-            const int col = kk * 16 + 2 * t4;
-            qf[kk][0] = g < heads ? *reinterpret_cast<const uint32_t*>(q + g * D + col) : 0u;
-            qf[kk][2] = g < heads ? *reinterpret_cast<const uint32_t*>(q + g * D + col + 8) : 0u;
-            if (GT == 16) {
-                qf[kk][1] = g + 8 < heads ? *reinterpret_cast<const uint32_t*>(q + (g + 8) * D + col) : 0u;
-                qf[kk][3] = g + 8 < heads ? *reinterpret_cast<const uint32_t*>(q + (g + 8) * D + col + 8) : 0u;
-            } else {
-                qf[kk][1] = qf[kk][3] = 0u;
-            }
-        }
-#pragma unroll
-        for (int n = 0; n < D / 8; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
-        m[0] = m[1] = -INFINITY;
-        l[0] = l[1] = 0.f;
-    };
+    // Rows shared with other CTAs: one begun before this CTA's part, one going on
+    // after it.  Their first place in the list (-1: none) and tiles; sequence and row.
+    int begun_first = -1, open_first = -1;
+    int begun_tiles = 0, begun_b = 0, begun_row = 0, open_tiles = 0, open_b = 0, open_row = 0;
+    const bool silent = cta == 0 && a.ctrl->pad[kCtrlInjectWord];   // the failure-detection test hook
+    uint32_t take = ring_u;        // the next unit to use
 
-    int seg_first = at.tile;   // first tile of the row that this CTA has
-    start_row();
-    for (int i = 0; i < items; ++i) {
-        cp_async_wait<S - 2>();
-        __syncwarp();
-        if (loaded < items) {
-            load((i + S - 1) % S);
-            next_place(a, rows, ld);
-            ++loaded;
-            if (loaded < items) look_up();
-        } else {
-            cp_async_commit();
+    // One turn a unit, the first S of them only to fill the ring: a single copy of
+    // the loading code, as this kernel runs through much of its code just once.
+    int first_place = (int)place - at.tile;   // of at's row in the list
+    int first = at.tile;           // of the row, in this CTA
+    int heads = 0, head0 = 0;
+    bool fresh = true;             // a row begins
+    uint32_t hi[NB][2], lo[NB][2]; // P^T of tokens 0..7 and 8..15: 16 bits, and what they leave
+    auto start_row = [&]() {
+        const int kvh = at.row / a.head_blocks, hb = at.row - kvh * a.head_blocks;
+        heads = min(kHeads, a.group - hb * kHeads);
+        head0 = kvh * a.group + hb * kHeads;
+        first = at.tile;
+#pragma unroll
+        for (int n = 0; n < NB; ++n) {
+#pragma unroll
+            for (int j = 0; j < D / 16; ++j) o[n][j][0] = o[n][j][1] = o[n][j][2] = o[n][j][3] = 0.f;
+            m[n][0] = m[n][1] = -INFINITY;
+            l[n][0] = l[n][1] = 0.f;
+#pragma unroll
+            for (int r = 0; r < 2; ++r) hi[n][r] = lo[n][r] = 0u;
         }
-        const int kvh = at.row / a.head_blocks, hb = at.row % a.head_blocks;
-        const int heads = min(kHeads, a.group - hb * kHeads);
-        const int head0 = kvh * a.group + hb * kHeads;
-        const int t0 = at.tile * kTile + warp * kSub;
-        const uint32_t kb = ring_u + (i % S) * STAGE, vb = kb + HALF;
-        if (t0 < at.len) {
-            // two accumulators for each half of the tokens: shorter chains
-            float s[2][2][4] = {};
-            {
-                const int token = (lane >> 4) * 8 + (lane & 7), half = (lane >> 3) & 1;
-                const uint32_t addr = kb + token * ROW;
+    };
+    // The end of a row's tiles here: the warps' results meet, under a common maximum,
+    // outputs added in warp order through the unit that has just been used.
+    auto finish_row = [&](bool row_ends) {
+        Place nx = at;
+        next_row(lens, n_seqs, rows, nx);
+        if (place < end) load_q(nx);    // there by the time the next row begins
 #pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk) {
-                    uint32_t bfr[4];
-                    ldsm4(bfr, addr + (((kk * 2 + half) ^ (token & 7)) << 4));
-                    Elem<T>::mma(s[kk & 1][0], qf[kk], bfr[0], bfr[1]);
-                    Elem<T>::mma(s[kk & 1][1], qf[kk], bfr[2], bfr[3]);
+        for (int n = 0; n < NB; ++n)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+#pragma unroll
+                for (int x = 4; x < 32; x <<= 1) l[n][c] += __shfl_xor_sync(0xffffffffu, l[n][c], x);
+                if (g == 0) {
+                    sh_m[warp][n * 8 + 2 * t4 + c] = m[n][c];
+                    sh_l[warp][n * 8 + 2 * t4 + c] = l[n][c];
                 }
             }
-            float x[2][4];
+        const bool whole = row_ends && first == 0;
+        const int64_t slot = (int64_t)(cta * 2 + (first == 0 ? 1 : 0)) * kHeads;
+        const uint32_t here = take - ring_u;
+        float* buf = reinterpret_cast<float*>(ring + here) + 2 * t4 * (D + 4) + g;   // [8][D + 4]: no bank twice
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
+        for (int n = 0; n < NB; ++n) {
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int t = t0 + j * 8 + 2 * t4 + (e & 1);
-                    x[j][e] = t < at.len ? (s[0][j][e] + s[1][j][e]) * a.scale_log2 : -INFINITY;
-                }
-            if (a.scores) {
-#pragma unroll
-                for (int r = 0; r < GT / 8; ++r)
-                    if (g + r * 8 < heads) {
-                        float* p = a.scores + ((int64_t)at.b * a.n_q_heads + head0 + g + r * 8) * a.score_stride + t0 + 2 * t4;
-                        *reinterpret_cast<float2*>(p) = make_float2(x[0][2 * r], x[0][2 * r + 1]);
-                        *reinterpret_cast<float2*>(p + 8) = make_float2(x[1][2 * r], x[1][2 * r + 1]);
-                    }
-            }
-            // The maximum that the exponents are taken against follows the true one
-            // only when it is exceeded by more than 2^8: fp32 sums hold the range, and
-            // the output is rescaled a few times a row instead of at every tile.
-            float top[2];
-            bool grow = false;
-#pragma unroll
-            for (int r = 0; r < GT / 8; ++r) {
-                float v = fmaxf(fmaxf(x[0][2 * r], x[0][2 * r + 1]), fmaxf(x[1][2 * r], x[1][2 * r + 1]));
-                v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
-                v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
-                top[r] = v;
-                grow |= v > m[r] + kLazyRescale || (m[r] == -INFINITY && v > -INFINITY);
-            }
-            if (__any_sync(0xffffffffu, grow)) {
-#pragma unroll
-                for (int r = 0; r < GT / 8; ++r) {
-                    const float to = fmaxf(m[r], top[r]);
-                    const float f = m[r] == -INFINITY ? 0.f : ex2(m[r] - to);
-                    m[r] = to;
-                    l[r] *= f;
-#pragma unroll
-                    for (int n = 0; n < D / 8; ++n) {
-                        o[n][2 * r] *= f;
-                        o[n][2 * r + 1] *= f;
-                        if (GT == 8) { o[n][2] *= f; o[n][3] *= f; }
-                    }
-                }
-            }
-            uint32_t hi[4], lo[4];
-#pragma unroll
-            for (int r = 0; r < GT / 8; ++r) {
-                const float ref = m[r] == -INFINITY ? 0.f : m[r];
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const float p0 = ex2(x[j][2 * r] - ref), p1 = ex2(x[j][2 * r + 1] - ref);
-                    l[r] += p0 + p1;
-                    const uint32_t h = Elem<T>::pack(p0, p1);
-                    const float2 back = Elem<T>::unpack(h);
-                    hi[j * 2 + r] = h;
-                    lo[j * 2 + r] = Elem<T>::pack(p0 - back.x, p1 - back.y);
-                }
-            }
-            if (GT == 8) { hi[1] = lo[0]; hi[3] = lo[2]; }
-            {
-                const int token = ((lane >> 3) & 1) * 8 + (lane & 7), half = lane >> 4;
-                const uint32_t addr = vb + token * ROW;
+            for (int c = 0; c < 2; ++c)
 #pragma unroll
                 for (int j = 0; j < D / 16; ++j) {
-                    uint32_t bfr[4];
-                    ldsm4_t(bfr, addr + (((j * 2 + half) ^ (token & 7)) << 4));
-                    Elem<T>::mma(o[2 * j], hi, bfr[0], bfr[1]);
-                    Elem<T>::mma(o[2 * j + 1], hi, bfr[2], bfr[3]);
-                    if (GT == 16) {
-                        Elem<T>::mma(o[2 * j], lo, bfr[0], bfr[1]);
-                        Elem<T>::mma(o[2 * j + 1], lo, bfr[2], bfr[3]);
-                    }
+                    buf[c * (D + 4) + j * 16] = o[n][j][c];
+                    buf[c * (D + 4) + j * 16 + 8] = o[n][j][c + 2];
                 }
-            }
-        }
-
-        const bool row_ends = at.tile == at.tiles - 1;
-        if (row_ends || i == items - 1) {
-            // the warps' results meet: common maximum, then outputs added in warp order
-            // through the stage that this tile has just left
-#pragma unroll
-            for (int r = 0; r < GT / 8; ++r) {
-                l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
-                l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
-                if (t4 == 0) { sh_m[warp][g + 8 * r] = m[r]; sh_l[warp][g + 8 * r] = l[r]; }
-            }
             __syncthreads();
-            float* mine = reinterpret_cast<float*>(ring + (i % S) * STAGE);
-#pragma unroll
-            for (int r = 0; r < GT / 8; ++r) {
-                float M = sh_m[0][g + 8 * r];
-#pragma unroll
-                for (int w = 1; w < kAttWarps; ++w) M = fmaxf(M, sh_m[w][g + 8 * r]);
-                const float f = m[r] == -INFINITY ? 0.f : ex2(m[r] - M);
-#pragma unroll
-                for (int n = 0; n < D / 8; ++n) {
-                    float v0 = o[n][2 * r], v1 = o[n][2 * r + 1];
-                    if (GT == 8) { v0 += o[n][2]; v1 += o[n][3]; }
-                    const int col = (n * 8 + 2 * t4) ^ ((g & 3) * 8);
-                    *reinterpret_cast<float2*>(mine + (g + 8 * r) * D + col) = make_float2(v0 * f, v1 * f);
-                }
-            }
-            __syncthreads();
-            const bool whole = row_ends && seg_first == 0;
-            const int slot = cta * 2 + (seg_first == 0 ? 1 : 0);
-            for (int e = threadIdx.x; e < heads * (D / 2); e += kAttThreads) {
-                const int h = e / (D / 2), col = (e % (D / 2)) * 2;
-                float M = sh_m[0][h];
+            const int quads = min(8, heads - n * 8) * (D / 4);
+#pragma unroll 1
+            for (int e = threadIdx.x; e < quads; e += kAttThreads) {
+                const int h8 = e / (D / 4), col = (e % (D / 4)) * 4, h = n * 8 + h8;
+                float M = sh_m[0][h], L = 0.f;
 #pragma unroll
                 for (int w = 1; w < kAttWarps; ++w) M = fmaxf(M, sh_m[w][h]);
-                float L = 0.f, v0 = 0.f, v1 = 0.f;
+                float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+                const float* from = reinterpret_cast<const float*>(smem + here) + h8 * (D + 4) + col;
 #pragma unroll
-                for (int w = 0; w < kAttWarps; ++w) {
-                    const float mw = sh_m[w][h];
-                    L += sh_l[w][h] * (mw == -INFINITY ? 0.f : ex2(mw - M));
-                    const float2 v = *reinterpret_cast<const float2*>(
-                        reinterpret_cast<const float*>(smem + (w * S + i % S) * STAGE) + h * D + (col ^ ((h & 3) * 8)));
-                    v0 += v.x;
-                    v1 += v.y;
+                for (int w = 0; w < kAttWarps; ++w, from += S * UNIT / 4) {
+                    // a warp without a score above -inf: 0, or NaN where it has met one
+                    const float f = sh_m[w][h] == -INFINITY ? (sh_l[w][h] == 0.f ? 0.f : NAN) : ex2(sh_m[w][h] - M);
+                    const float4 p = *reinterpret_cast<const float4*>(from);
+                    L += sh_l[w][h] * f;
+                    v.x += p.x * f; v.y += p.y * f; v.z += p.z * f; v.w += p.w * f;
                 }
                 if (whole) {
-                    // no token, or none with a score above -inf: zeros
-                    const float inv = M == -INFINITY && L == 0.f ? 0.f : 1.f / L;
-                    *reinterpret_cast<uint32_t*>(a.out + at.b * a.out_stride + (int64_t)(head0 + h) * D + col) =
-                        Elem<T>::pack(v0 * inv, v1 * inv);
-                    if (col == 0) {
-                        const float lse2 = M == -INFINITY && L == 0.f ? -INFINITY : M + log2f(L);
-                        const int64_t at_h = (int64_t)at.b * a.n_q_heads + head0 + h;
-                        if (a.lse) a.lse[at_h] = lse2 * kLn2;
-                        if (a.scores) a.lse2[at_h] = lse2;
-                    }
+                    const bool none = M == -INFINITY && L == 0.f;
+                    const float inv = none ? 0.f : 1.f / L;
+                    *reinterpret_cast<uint2*>(a.out + at.b * a.out_stride + (int64_t)(head0 + h) * D + col) =
+                        make_uint2(Elem<T>::pack(v.x * inv, v.y * inv), Elem<T>::pack(v.z * inv, v.w * inv));
+                    if (col == 0) write_lse(a, at.b, head0 + h, M, L, none);
                 } else {
-                    *reinterpret_cast<float2*>(a.part_o + ((int64_t)slot * kHeads + h) * D + col) = make_float2(v0, v1);
-                    if (col == 0)
-                        *reinterpret_cast<float2*>(a.part_ml + ((int64_t)slot * kHeads + h) * 2) = make_float2(M, L);
+                    __stcg(reinterpret_cast<float4*>(a.part_o + (slot + h) * D + col), v);
+                    if (col == 0) __stcg(reinterpret_cast<float2*>(a.part_ml + (slot + h) * 2), make_float2(M, L));
                 }
             }
             __syncthreads();
         }
-        next_place(a, rows, at);
-        if (row_ends && i + 1 < items) {
-            seg_first = 0;
-            start_row();
-        }
-    }
-}
-
-// Adds up the partial results of the rows that cross CTAs.  Block x stands for
-// row x where there are fewer rows than parts, else for the border between
-// parts x - 1 and x (each split row is done by the first border inside it);
-// blocks of y share the row's heads.
-constexpr int kJoinThreads = 256;
-template <typename T, int D>
-__global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(const AttendArgs a, int attend_ctas, int by_row) {
-    constexpr int LANES = D / 4, WAYS = kJoinThreads / LANES;
-    __shared__ float sh_f[kMaxCtas + 1];
-    __shared__ float sh_red[8];
-    __shared__ float4 sh_o[WAYS][LANES];
-    griddep_wait();
-    const int rows = a.c.n_kv_heads * a.head_blocks;
-    Shares sh;
-    sh.total = warp_tiles(a, a.c.n_seqs) * rows;
-    sh.parts = (int)min((int64_t)attend_ctas, sh.total);
-    int b, row, tiles;
-    int64_t first;   // first tile of the row
-    if (by_row) {
-        b = blockIdx.x / rows;
-        row = blockIdx.x % rows;
-        tiles = tiles_of(checked_len(a, b));
-        first = warp_tiles(a, b) * rows + (int64_t)row * tiles;
-    } else {
-        const int c = blockIdx.x;
-        if (c < 1 || c >= sh.parts) return;
-        const int64_t x = sh.start(c);
-        find_seq(a, rows, x, b, first);
-        tiles = tiles_of(checked_len(a, b));
-        row = (int)((x - first) / tiles);
-        first += (int64_t)row * tiles;
-        if (first == x || sh.start(c - 1) > first) return;   // no row cut here, or not its first cut
-    }
-    const int c0 = sh.owner(first), c1 = sh.owner(first + tiles - 1), parts = c1 - c0 + 1;
-    if (parts == 1) return;
-    const int kvh = row / a.head_blocks, hb = row % a.head_blocks;
-    const int heads = min(kHeads, a.group - hb * kHeads);
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    for (int h = blockIdx.y; h < heads; h += gridDim.y) {
-        auto slot = [&](int i) { return (int64_t)((c0 + i) * 2 + (i == 0 ? 1 : 0)) * kHeads + h; };
-        float M = -INFINITY;
-        for (int i = tid; i < parts; i += kJoinThreads) M = fmaxf(M, a.part_ml[slot(i) * 2]);
-#pragma unroll
-        for (int off = 16; off; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
-        if (lane == 0) sh_red[warp] = M;
-        __syncthreads();
-#pragma unroll
-        for (int w = 0; w < kJoinThreads / 32; ++w) M = fmaxf(M, sh_red[w]);
-        __syncthreads();
-        float L = 0.f;
-        for (int i = tid; i < parts; i += kJoinThreads) {
-            const float2 ml = *reinterpret_cast<const float2*>(a.part_ml + slot(i) * 2);
-            const float f = ml.x == -INFINITY ? 0.f : ex2(ml.x - M);
-            sh_f[i] = f;
-            L += ml.y * f;
-        }
-        L = warp_sum(L);
-        if (lane == 0) sh_red[warp] = L;
-        __syncthreads();
-        L = 0.f;
-#pragma unroll
-        for (int w = 0; w < kJoinThreads / 32; ++w) L += sh_red[w];
-        const int col = tid % LANES, way = tid / LANES;
-        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-        for (int i = way; i < parts; i += WAYS) {
-            const float4 p = *reinterpret_cast<const float4*>(a.part_o + slot(i) * D + col * 4);
-            const float f = sh_f[i];
-            v.x += p.x * f; v.y += p.y * f; v.z += p.z * f; v.w += p.w * f;
-        }
-        sh_o[way][col] = v;
-        __syncthreads();
-        const int head = kvh * a.group + hb * kHeads + h;
-        const bool none = M == -INFINITY && L == 0.f;
-        if (way == 0) {
-#pragma unroll
-            for (int w = 1; w < WAYS; ++w) {
-                const float4 p = sh_o[w][col];
-                v.x += p.x; v.y += p.y; v.z += p.z; v.w += p.w;
+        if (!whole) {
+            const int from = first_place;
+            if (first == 0) {
+                open_first = from;
+                open_tiles = at.tiles; open_b = at.b; open_row = at.row;
+            } else {
+                begun_first = from;
+                begun_tiles = at.tiles; begun_b = at.b; begun_row = at.row;
             }
-            const float inv = none ? 0.f : 1.f / L;
-            uint2 u = make_uint2(Elem<T>::pack(v.x * inv, v.y * inv), Elem<T>::pack(v.z * inv, v.w * inv));
-            *reinterpret_cast<uint2*>(a.out + b * a.out_stride + (int64_t)head * D + col * 4) = u;
+            if (threadIdx.x == 0 && !silent) atomic_add_release_gpu(&a.sync[sh.owner(from)].arrived, 1);
         }
-        if (tid == 0) {
-            const float lse2 = none ? -INFINITY : M + log2f(L);
-            const int64_t at_h = (int64_t)b * a.n_q_heads + head;
-            if (a.lse) a.lse[at_h] = lse2 * kLn2;
-            if (a.scores) a.lse2[at_h] = lse2;
+        at = nx;
+        first_place = (int)place;
+        fresh = true;
+    };
+#pragma unroll 1
+    for (int u = -S; u < 0 || place < end || (u & 1); ++u) {
+        if (fresh && u >= 0) {
+            start_row();
+            fresh = false;
         }
-        __syncthreads();
+        const int t0 = at.tile * kTile + warp * kSub;
+        const bool mine = u >= 0 && t0 < at.len;
+        cp_async_wait<S - 1>();
+        __syncwarp();
+        if (mine && !(u & 1)) {
+            // S^T = K q^T: 16 tokens by 8 heads a block, two chains of accumulators
+            float s[NB][2][4];
+            {
+#pragma unroll
+                for (int n = 0; n < NB; ++n)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) s[n][0][e] = s[n][1][e] = 0.f;
+                uint32_t from[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) from[j] = take + k_lane[j];
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk) {
+                    uint32_t k4[4];
+                    ldsm4(k4, from[kk & 3] + (kk >> 2) * 128);
+#pragma unroll
+                    for (int n = 0; n < NB; ++n) Elem<T>::mma(s[n][kk & 1], k4, qf[n][kk][0], qf[n][kk][1]);
+                }
+            }
+            {
+                bool grow = false;
+                // s[n][0][2r + c] becomes the score of token g + 8r with head 2 t4 + c
+#pragma unroll
+                for (int n = 0; n < NB; ++n)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) s[n][0][e] = (s[n][0][e] + s[n][1][e]) * a.scale_log2;
+                if (t0 + kSub > at.len) {
+#pragma unroll
+                    for (int n = 0; n < NB; ++n)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            if (t0 + g + 8 * (e >> 1) >= at.len) s[n][0][e] = -INFINITY;
+                }
+                if (a.scores) {
+#pragma unroll
+                    for (int n = 0; n < NB; ++n)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int h = n * 8 + 2 * t4 + (e & 1), t = t0 + g + 8 * (e >> 1);
+                            if (h < heads && t < at.len)
+                                a.scores[((int64_t)at.b * a.n_q_heads + head0 + h) * a.score_stride + t] = s[n][0][e];
+                        }
+                }
+                // The maximum that the exponents are taken against follows the true one
+                // only when it is exceeded by more than 2^8: fp32 sums hold the range, and
+                // the maximum is found and the output rescaled a few times a row.
+#pragma unroll
+                for (int n = 0; n < NB; ++n)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) grow |= s[n][0][e] > m[n][e & 1] + kLazyRescale;
+                if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+                    for (int n = 0; n < NB; ++n)
+#pragma unroll
+                        for (int c = 0; c < 2; ++c) {
+                            float to = fmaxf(m[n][c], fmaxf(s[n][0][c], s[n][0][c + 2]));
+#pragma unroll
+                            for (int x = 4; x < 32; x <<= 1) to = fmaxf(to, __shfl_xor_sync(0xffffffffu, to, x));
+                            const float f = m[n][c] == -INFINITY ? 0.f : ex2(m[n][c] - to);
+                            m[n][c] = to;
+                            l[n][c] *= f;
+#pragma unroll
+                            for (int j = 0; j < D / 16; ++j) {
+                                o[n][j][c] *= f;
+                                o[n][j][c + 2] *= f;
+                            }
+                        }
+                }
+                // Probabilities enter the product as two 16-bit terms, about 16 (bf16) or 22
+                // (fp16) bits: one alone would cost as much accuracy as the output's rounding.
+#pragma unroll
+                for (int n = 0; n < NB; ++n) {
+                    const float r0 = m[n][0] == -INFINITY ? 0.f : m[n][0], r1 = m[n][1] == -INFINITY ? 0.f : m[n][1];
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        const float p0 = ex2(s[n][0][2 * r] - r0), p1 = ex2(s[n][0][2 * r + 1] - r1);
+                        l[n][0] += p0;
+                        l[n][1] += p1;
+                        const uint32_t h = Elem<T>::pack(p0, p1);
+                        const float2 back = Elem<T>::unpack(h);
+                        hi[n][r] = transpose8(h);
+                        lo[n][r] = transpose8(Elem<T>::pack(p0 - back.x, p1 - back.y));
+                    }
+                }
+            }
+        } else if (mine) {
+            // O^T += V^T P^T: 16 dimensions by 8 heads a block
+            uint32_t from[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) from[j] = take + v_lane[j];
+#pragma unroll
+            for (int j = 0; j < D / 16; ++j) {
+                uint32_t v4[4];
+                ldsm4_t(v4, from[j & 3] + (j >> 2) * 128);
+#pragma unroll
+                for (int n = 0; n < NB; ++n) {
+                    Elem<T>::mma(o[n][j], v4, hi[n][0], hi[n][1]);
+                    Elem<T>::mma(o[n][j], v4, lo[n][0], lo[n][1]);
+                }
+            }
+        }
+        __syncwarp();
+        const bool row_ends = at.tile == at.tiles - 1;
+        if (u >= 0 && (u & 1)) {
+            place += row_ends ? 1 + kRowCost : 1;
+            if (row_ends || place >= end) finish_row(row_ends);
+            else ++at.tile;
+        }
+        load_unit();
+        if (u >= 0) take = take + UNIT == ring_end ? ring_u : take + UNIT;
+    }
+    cp_async_wait<0>();
+    griddep_launch_dependents();
+
+    // the rows shared with other CTAs
+    if (begun_first >= 0) {
+        const int c0 = sh.owner(begun_first), parts = sh.owner(begun_first + begun_tiles - 1) - c0 + 1;
+        if (!join_row<T, D>(a, smem, begun_b, begun_row, c0, parts, cta - c0)) return;
+    }
+    if (open_first >= 0) {
+        const int parts = sh.owner(open_first + open_tiles - 1) - cta + 1;
+        join_row<T, D>(a, smem, open_b, open_row, cta, parts, 0);
     }
 }
 
@@ -558,15 +745,18 @@ __global__ void __launch_bounds__(kWeightThreads) attend_weight_kernel(const Att
 }
 
 struct AttendWs {
-    size_t part_o, part_ml, lse2, scores, total;
+    size_t sync, part_o, part_ml, lse2, scores, total;
     int64_t score_stride;
 };
 static AttendWs attend_ws(const moe_w4_kv_cache& c, int n_q_heads, int max_len, bool track) {
     AttendWs w{};
-    size_t o = MOE_W4_CTRL_BYTES;
+    // the arrival records come first, where no other operator writes: they have to
+    // be zero between calls
+    size_t o = MOE_W4_CTRL_BYTES + kSyncBytes;
     auto take = [&](size_t bytes) { const size_t at = o; o += round_up(bytes, 256); return at; };
-    w.part_o = take((size_t)2 * kMaxCtas * kHeads * c.head_dim * 4);
-    w.part_ml = take((size_t)2 * kMaxCtas * kHeads * 2 * 4);
+    w.sync = MOE_W4_CTRL_BYTES;
+    w.part_o = take((size_t)2 * most_ctas(c.head_dim) * kHeads * c.head_dim * 4);
+    w.part_ml = take((size_t)2 * most_ctas(c.head_dim) * kHeads * 2 * 4);
     w.score_stride = (int64_t)round_up((size_t)max_len, kSub);
     if (track) {
         w.lse2 = take((size_t)c.n_seqs * n_q_heads * 4);
@@ -581,24 +771,42 @@ static cudaError_t launch_attend(const AttendArgs& a, cudaStream_t st) {
     int dev = 0;
     const int sms = sm_count(&dev);
     if (sms < 1) return cudaErrorInvalidDevice;
-    constexpr int smem = AttCfg<D>::stages * kAttWarps * 2 * kSub * D * 2;
+    constexpr int ring = AttCfg<D>::slots * kAttWarps * unit_bytes(D);
+    // a join holds parts * cols < kHeads * D / 4 + parts columns, and parts * pairs <=
+    // kHeads / 2 + 2 parts maxima and sums
+    static_assert(ring >= 16 * (kHeads / 2 + 3 * most_ctas(D) + kHeads * D / 4), "a join fits the ring");
+    static_assert(most_ctas(D) * sizeof(RowSync) <= kSyncBytes, "a record for every CTA");
     const int64_t rows = (int64_t)a.c.n_seqs * a.c.n_kv_heads * a.head_blocks;
-    // no more CTAs than tiles the longest lengths could make
-    const int64_t most = rows * ((a.max_len + kTile - 1) / kTile > 0 ? (a.max_len + kTile - 1) / kTile : 1);
-    int64_t ctas = (int64_t)sms * AttCfg<D>::ctas;
-    if (ctas > kMaxCtas) ctas = kMaxCtas;
+    // no more CTAs than places that the longest lengths could make
+    const int64_t tiles = a.max_len > kTile ? (a.max_len + kTile - 1) / kTile : 1, most = rows * (tiles + kRowCost);
+    // the lengths of very many sequences cost a CTA of an SM
+    const int smem = ring + (int)round_up((size_t)a.c.n_seqs * 4, 16);
+    const int per_sm = (228 << 10) / (smem + 2304) < AttCfg<D>::ctas ? (228 << 10) / (smem + 2304) : AttCfg<D>::ctas;
+    int64_t ctas = (int64_t)sms * per_sm;
+    if (ctas > most_ctas(D)) ctas = most_ctas(D);
     if (ctas > most) ctas = most;
     static std::atomic<unsigned> ready[2];
-    auto kern = a.group <= 8 ? attend_kernel<T, D, 8> : attend_kernel<T, D, 16>;
-    cudaError_t e = allow_smem((const void*)kern, smem, ready[a.group <= 8 ? 0 : 1], dev);
-    if (e == cudaSuccess) e = launch_pdl(true, kern, dim3((unsigned)ctas), dim3(kAttThreads), smem, st, a);
-    // rows can only be cut where there are fewer rows than tiles
-    if (e == cudaSuccess && ctas > 1 && most > rows) {
-        const int by_row = rows <= ctas;
-        const int heads = a.group < kHeads ? a.group : kHeads;
-        e = launch_pdl(true, attend_join_kernel<T, D>, dim3((unsigned)(by_row ? rows : ctas), by_row ? heads : 1),
-                       dim3(kJoinThreads), 0, st, a, (int)ctas, by_row);
-    }
+    auto kern = a.group <= 8 ? attend_kernel<T, D, 1> : attend_kernel<T, D, 2>;
+    cudaError_t e = allow_smem((const void*)kern, ring + MOE_W4_MAX_SEQS * 4, ready[a.group <= 8 ? 0 : 1], dev);
+    if (e != cudaSuccess) return e;
+    // Rows can be cut only where there are more tiles than rows; CTAs that share a
+    // row wait for one another, so all must be resident.
+    const bool together = ctas > 1 && tiles > 1;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeCooperative;
+    attr[1].val.cooperative = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.blockDim = dim3(kAttThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cfg.attrs = attr;
+    cfg.numAttrs = together ? 2 : 1;
+    do {   // a device shared with others may refuse a full grid: any smaller one will do
+        cfg.gridDim = dim3((unsigned)ctas);
+        e = cudaLaunchKernelEx(&cfg, kern, a);
+    } while (e == cudaErrorCooperativeLaunchTooLarge && (cudaGetLastError(), ctas /= 2) > 0);
     if (e == cudaSuccess && a.scores && a.max_len > 0)
         e = launch_pdl(true, attend_weight_kernel,
                        dim3((a.max_len + kWeightThreads - 1) / kWeightThreads, a.c.n_kv_heads, a.c.n_seqs),
@@ -659,7 +867,14 @@ int moe_w4_attend_decode(const moe_w4_kv_cache* c, int n_q_heads, const void* q,
     a.scale_log2 = scale * kLog2e;
     a.part_o = reinterpret_cast<float*>(ws + w.part_o);
     a.part_ml = reinterpret_cast<float*>(ws + w.part_ml);
-    a.status = reinterpret_cast<unsigned int*>(ws);
+    a.ctrl = reinterpret_cast<Ctrl*>(ws);
+    a.sync = reinterpret_cast<RowSync*>(ws + w.sync);
+    a.k = static_cast<const uint4*>(c->k);
+    a.v = static_cast<const uint4*>(c->v);
+    a.page_pieces = (uint32_t)(c->page_stride / 8);
+    a.head_pieces = (uint32_t)(c->head_stride / 8);
+    a.slot_pieces = (uint32_t)(c->slot_stride / 8);
+    a.runs = c->page_size % kSub == 0;
     if (track) {
         a.lse2 = reinterpret_cast<float*>(ws + w.lse2);
         a.scores = reinterpret_cast<float*>(ws + w.scores);
@@ -669,6 +884,8 @@ int moe_w4_attend_decode(const moe_w4_kv_cache* c, int n_q_heads, const void* q,
         a.track_seq = track->seq_stride;
         a.track_head = track->head_stride;
     }
+    const int64_t places = ((max_len > kTile ? ((int64_t)max_len + kTile - 1) / kTile : 1) + kRowCost) * c->n_seqs * c->n_kv_heads;
+    if (places > INT_MAX / a.head_blocks) return MOE_W4_ERR_UNSUPPORTED;   // the list is indexed with 32 bits
     return launched(c->dtype == MOE_W4_TYPE_BF16 ? launch_attend_dim<__nv_bfloat16>(c->head_dim, a, stream)
                                                  : launch_attend_dim<__half>(c->head_dim, a, stream));
 }

@@ -282,7 +282,7 @@ static size_t evict_list_bytes(const moe_w4_kv_cache& c, int budget) {
     return round_up(evict_rows(c) * (size_t)budget * 4, 256);
 }
 static size_t evict_bytes(const moe_w4_kv_cache& c, int budget) {
-    return MOE_W4_CTRL_BYTES + 2 * evict_list_bytes(c, budget) + round_up(evict_rows(c) * 4, 256);
+    return MOE_W4_CTRL_BYTES + kSyncBytes + 2 * evict_list_bytes(c, budget) + round_up(evict_rows(c) * 4, 256);
 }
 
 }  // namespace mw4
@@ -370,9 +370,9 @@ int moe_w4_kv_evict(const moe_w4_kv_cache* c, const moe_w4_kv_track* track, cons
     a.chunks = c->head_dim / 8;
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     const size_t list = evict_list_bytes(*c, places);
-    a.src = reinterpret_cast<int32_t*>(ws + MOE_W4_CTRL_BYTES);
-    a.movers = reinterpret_cast<int32_t*>(ws + MOE_W4_CTRL_BYTES + list);
-    a.kept = reinterpret_cast<int32_t*>(ws + MOE_W4_CTRL_BYTES + 2 * list);
+    a.src = reinterpret_cast<int32_t*>(ws + MOE_W4_CTRL_BYTES + kSyncBytes);
+    a.movers = reinterpret_cast<int32_t*>(ws + MOE_W4_CTRL_BYTES + kSyncBytes + list);
+    a.kept = reinterpret_cast<int32_t*>(ws + MOE_W4_CTRL_BYTES + kSyncBytes + 2 * list);
     a.status = reinterpret_cast<unsigned int*>(ws);
     const size_t smem = (size_t)a.key_room * 4;
     static std::atomic<unsigned> ready;

@@ -63,6 +63,7 @@ inline int check_cache(const moe_w4_kv_cache* c, bool need_lens) {
     if (c->head_dim != 64 && c->head_dim != 128 && c->head_dim != 256) return MOE_W4_ERR_UNSUPPORTED;
     if (c->n_seqs > MOE_W4_MAX_SEQS || c->n_kv_heads > 1024) return MOE_W4_ERR_UNSUPPORTED;
     if ((int64_t)c->pages_per_seq * c->page_size > (1 << 30)) return MOE_W4_ERR_UNSUPPORTED;
+    if (((c->page_stride | c->head_stride | c->slot_stride) >> 3) > UINT32_MAX) return MOE_W4_ERR_UNSUPPORTED;
     if (c->n_seqs == 0) return MOE_W4_OK;
     if (!c->k || !c->v || !c->block_table || (need_lens && !c->seq_lens)) return MOE_W4_ERR_INVALID;
     if (misaligned(c->k, 16) || misaligned(c->v, 16) || c->page_stride % 8 || c->head_stride % 8 ||
@@ -88,7 +89,11 @@ inline KvView kv_view(const moe_w4_kv_cache& c) {
             c.pages_per_seq, c.n_seqs, c.n_kv_heads};
 }
 
-inline size_t round_up(size_t v, size_t to) { return (v + to - 1) / to * to; }
+// Bytes after the control header that hold the attention's arrival records; the
+// other operators keep off them, since they must be zero between calls.
+constexpr int kSyncBytes = 8192;
+
+__host__ __device__ constexpr size_t round_up(size_t v, size_t to) { return (v + to - 1) / to * to; }
 
 // The current device and its SM count (asked once per device).
 inline int sm_count(int* device = nullptr) {

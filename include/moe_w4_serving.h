@@ -42,7 +42,7 @@ enum { MOE_W4_TYPE_BF16 = 0, MOE_W4_TYPE_FP16 = 1, MOE_W4_TYPE_FP32 = 2 };
  * not read.
  * Supported: dtype bf16 or fp16; head_dim 64, 128 or 256; 1 <= n_kv_heads <=
  * 1024; page_size >= 1; 1 <= n_seqs <= MOE_W4_MAX_SEQS (0: every call returns
- * at once); strides non-negative multiples of 8, k and v 16-byte aligned;
+ * at once); strides non-negative multiples of 8 below 2^35, k and v 16-byte aligned;
  * pages_per_seq * page_size <= 2^30.
  * Sequences may share pages that calls only read (a common prefix); a page
  * that append or evict writes must belong to one sequence. */

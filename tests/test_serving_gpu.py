@@ -522,3 +522,19 @@ def test_logprobs_many_rows(torch, sv, rows):
     x = (torch.randn(rows, 5003, device="cuda", generator=g) * 3).to(torch.bfloat16)
     t = torch.randint(0, 5003, (rows,), device="cuda", generator=g).to(torch.int32)
     check_logprobs(torch, sv, x, t, 9)
+
+
+def test_attention_wait_timeout_is_reported(torch, sv):
+    """With the hook on, CTA 0 does not say that its partial result is there: the waits for it run out (2 s), the status
+    says so, and after the workspace is cleared the next call is right."""
+    from bit_quantized_sparse_gb300 import moe_w4 as mw
+    s = Setup(torch, sv, [4000], 1, 64, 16, seed=20)
+    q = s.randn(1, 4, 64).to(s.dt)
+    good = sv.attend_decode(s.cache, q)
+    (ptr, size, _), = s.cache._ws.values()
+    stream = torch.cuda.current_stream().cuda_stream
+    assert mw.moe_w4_test_skip_publish(ptr, size, 1, stream) == 0
+    sv.attend_decode(s.cache, q)
+    assert s.cache.status() == 1
+    assert mw.moe_w4_workspace_init(ptr, size, stream) == 0
+    assert torch.equal(sv.attend_decode(s.cache, q), good) and s.cache.status() == 0
