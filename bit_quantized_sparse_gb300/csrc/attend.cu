@@ -775,7 +775,7 @@ static cudaError_t launch_attend(const AttendArgs& a, cudaStream_t st) {
     // a join holds parts * cols < kHeads * D / 4 + parts columns, and parts * pairs <=
     // kHeads / 2 + 2 parts maxima and sums
     static_assert(ring >= 16 * (kHeads / 2 + 3 * most_ctas(D) + kHeads * D / 4), "a join fits the ring");
-    static_assert(most_ctas(D) * sizeof(RowSync) <= kSyncBytes, "a record for every CTA");
+    static_assert(most_ctas(D) * sizeof(RowSync) <= kRowSyncBytes, "a record for every CTA");
     const int64_t rows = (int64_t)a.c.n_seqs * a.c.n_kv_heads * a.head_blocks;
     // no more CTAs than places that the longest lengths could make
     const int64_t tiles = a.max_len > kTile ? (a.max_len + kTile - 1) / kTile : 1, most = rows * (tiles + kRowCost);

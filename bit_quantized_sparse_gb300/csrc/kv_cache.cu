@@ -64,6 +64,19 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const AppendA
 // ---------------------------------------------------------------------------
 // evict
 // ---------------------------------------------------------------------------
+// A row is a (sequence, head) and belongs to a cluster of 1 to 8 CTAs, each with
+// a contiguous range of its tokens:
+//   - the budget-th largest key T by three histogram passes over the key's
+//     digits, the CTAs' histograms added up through distributed shared memory;
+//   - which tokens stay (ties at T by index, ranks from the CTAs before), and
+//     two lists in ascending order: places below the budget that are dropped,
+//     tokens past it that are kept (as many);
+//   - the lists' pairs, shared out among the CTAs: keys, values, weight and
+//     position of the token move into the place.
+// A token moves from an index >= budget to one below it, so no place is both
+// read and written and any order is right.
+// Bytes bound it in principle (keys read once, moved rows read and written);
+// at these sizes the chain of cluster barriers does.
 struct EvictArgs {
     KvView c;
     const float* weight;
@@ -73,27 +86,31 @@ struct EvictArgs {
     int32_t* pos_out;
     int32_t* lens_out;
     int64_t track_seq, track_head;
-    int budget, sink, recent, max_len, key_room, chunks;
-    int32_t* src;      // [row][budget] where the token of each place comes from
-    int32_t* movers;   // [row][budget] kept tokens past the budget, ascending
-    int32_t* kept;     // [row] tokens of the row after the cut
+    int budget, sink, recent, max_len, key_room;
+    int32_t* holes;          // [row][budget]
+    int32_t* movers;         // [row][budget]
+    int32_t* moved;          // [row] pairs in the lists, or NULL: the selecting CTAs move them too
+    unsigned int* heads_in;  // [n_seqs] heads that have read the length; zero between calls
     unsigned int* status;
 };
 
-constexpr int kSelectThreads = 1024;
+constexpr int kEvictThreads = 1024, kEvictWarps = kEvictThreads / 32;
+constexpr int kEvictMaxCluster = 8;
 constexpr int kDigits = 3;                       // 11 + 11 + 10 bits of the key
-constexpr int kHistBins = 2048;
-constexpr int kKeyRoom = 48 * 1024;              // keys held in shared memory
-constexpr int kMoveThreads = 256;
+constexpr int kHistBins = 2048;                  // two bins a thread
+constexpr int kKeyRoom = 40 * 1024;              // keys that a CTA holds in shared memory
+constexpr int kEvictUnroll = 4;                  // row pieces in flight of a thread
+constexpr int64_t kInlineMoveBytes = 4 << 20;    // moved by the selecting CTAs, at most
+constexpr int kMovePairs = 64;                   // tokens moved at a time by a CTA
 
-MW4_DEV int block_sum_1024(int v, int* warp_sums) {   // every thread gets the sum
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    v = __reduce_add_sync(0xffffffffu, v);
-    __syncthreads();
-    if (lane == 0) warp_sums[warp] = v;
-    __syncthreads();
-    return __reduce_add_sync(0xffffffffu, warp_sums[lane]);
-}
+struct EvictShared {
+    int hist[kDigits][kHistBins];
+    int64_t from[kMovePairs], to[kMovePairs];
+    int warp_sums[kEvictWarps];
+    int holes, movers;       // of this CTA
+    uint32_t digit;
+    int above, n;
+};
 
 // Sum over the warps before this one of the warps' values (uniform in a warp).
 MW4_DEV int warps_before(int v, int* warp_sums) {
@@ -108,58 +125,116 @@ MW4_DEV int warps_before(int v, int* warp_sums) {
 // one that is kept by its position, the order-preserving bits of its weight
 // otherwise, 0 for NaN.  order_key of a number lies strictly between (of -inf
 // it is 0x007fffff, of +inf 0xff800000).
-MW4_DEV uint32_t evict_key(const EvictArgs& a, int64_t row, int j, int64_t oldest_recent) {
-    const int p = a.pos[row + j];
-    const float w = a.weight[row + j];
+MW4_DEV uint32_t evict_key(const EvictArgs& a, float w, int p, int64_t oldest_recent) {
     if (p < a.sink || p >= oldest_recent) return 0xffffffffu;
     return isnan(w) ? 0u : order_key(w + 0.f);   // -0 + 0 = +0
 }
 
-// One CTA per (sequence, head): the budget-th largest key by three histogram
-// passes over the key's digits, then the places it leaves and the tokens that
-// fill them, in ascending order of both.
-__global__ void __launch_bounds__(kSelectThreads) kv_evict_select_kernel(const EvictArgs a) {
+// Moves the tokens of `count` <= kMovePairs pairs of a row's lists: one thread
+// looks a pair's places up and moves its weight and position, then rows of LR
+// lanes copy keys and values, kEvictUnroll pieces of a thread in flight.
+template <int LR, int THREADS>
+MW4_DEV void move_pairs(const EvictArgs& a, int b, int h, int64_t row, const int32_t* holes, const int32_t* movers, int count,
+                        int64_t* sh_from, int64_t* sh_to) {
+    const int tid = threadIdx.x;
+    if (tid < count) {
+        const int src = movers[tid], dst = holes[tid];
+        const float w = a.weight[row + src];
+        const int p = a.pos[row + src];
+        int64_t from = kv_offset(a.c, b, src);
+        const int64_t to = kv_offset(a.c, b, dst);
+        if (from < 0 || to < 0) {
+            raise_status(a.status, MOE_W4_STATUS_BAD_INDEX);
+            from = -1;
+        }
+        sh_from[tid] = from;
+        sh_to[tid] = to;
+        a.weight_out[row + dst] = w;
+        a.pos_out[row + dst] = p;
+    }
+    __syncthreads();
+    // keys of pair i are copy 2 i, its values copy 2 i + 1
+    constexpr int PER = THREADS / LR;            // rows copied at a time
+    const int64_t in_row = h * a.c.head_stride + tid % LR * 8;
+    for (int x0 = tid / LR; x0 < 2 * count; x0 += PER * kEvictUnroll) {
+        uint4 v[kEvictUnroll];
+#pragma unroll
+        for (int k = 0; k < kEvictUnroll; ++k) {
+            const int x = x0 + k * PER;
+            if (x < 2 * count && sh_from[x >> 1] >= 0)
+                v[k] = *reinterpret_cast<const uint4*>((x & 1 ? a.c.v : a.c.k) + sh_from[x >> 1] + in_row);
+        }
+#pragma unroll
+        for (int k = 0; k < kEvictUnroll; ++k) {
+            const int x = x0 + k * PER;
+            if (x < 2 * count && sh_from[x >> 1] >= 0)
+                *reinterpret_cast<uint4*>(const_cast<uint16_t*>(x & 1 ? a.c.v : a.c.k) + sh_to[x >> 1] + in_row) = v[k];
+        }
+    }
+    __syncthreads();
+}
+
+template <int LR>   // lanes of a row of keys: head_dim / 8
+__global__ void __launch_bounds__(kEvictThreads) kv_evict_kernel(const EvictArgs a) {
     extern __shared__ uint32_t keys[];
-    __shared__ int hist[kHistBins];
-    __shared__ int warp_sums[32];
-    __shared__ uint32_t sh_digit;
-    __shared__ int sh_above;
+    __shared__ EvictShared sh;
     griddep_wait();
-    const int b = blockIdx.x / a.c.n_kv_heads, h = blockIdx.x % a.c.n_kv_heads;
+    griddep_launch_dependents();
+    const int ctas = (int)cluster_size(), rank = (int)cluster_rank(), r = blockIdx.x / ctas;
+    const int b = r / a.c.n_kv_heads, h = r % a.c.n_kv_heads;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    int n = a.c.lens[b];
-    if (n < 0 || n > a.max_len) {
-        if (tid == 0) raise_status(a.status, MOE_W4_STATUS_BAD_INDEX);
-        n = n < 0 ? 0 : a.max_len;
+    // one reading of the length for the whole cluster: its CTAs have to take the
+    // same turns, whatever happens to the length meanwhile
+    if (rank == 0 && tid == 0) {
+        const int x = a.c.lens[b];
+        if (x < 0 || x > a.max_len) raise_status(a.status, MOE_W4_STATUS_BAD_INDEX);
+        sh.n = x < 0 ? 0 : min(x, a.max_len);
     }
-    int32_t* src = a.src + (int64_t)blockIdx.x * a.budget;
-    int32_t* movers = a.movers + (int64_t)blockIdx.x * a.budget;
-    if (tid == 0) a.kept[blockIdx.x] = min(n, a.budget);
-    if (n <= a.budget) {
-        for (int j = tid; j < n; j += kSelectThreads) src[j] = j;
-        return;
-    }
+    for (int i = tid; i < kDigits * kHistBins; i += kEvictThreads) (&sh.hist[0][0])[i] = 0;
+    auto sync = [&]() {
+        if (ctas > 1) cluster_sync();
+        else __syncthreads();
+    };
+    sync();
+    const int n = ld_cluster(&sh.n, 0);
     const int64_t row = b * a.track_seq + h * a.track_head;
+    const bool copies = a.weight_out != a.weight || a.pos_out != a.pos;
+    // this CTA's tokens
+    const int span = ((n + ctas - 1) / ctas + 31) & ~31;
+    const int lo = min(n, rank * span), hi = min(n, lo + span);
+    const bool cut = n > a.budget;
     const int64_t oldest_recent = (int64_t)a.seen[b] - a.recent;
-    const bool held = n <= a.key_room;
-    if (held)
-        for (int j = tid; j < n; j += kSelectThreads) keys[j] = evict_key(a, row, j, oldest_recent);
-    auto key = [&](int j) { return held ? keys[j] : evict_key(a, row, j, oldest_recent); };
+    const bool held = span <= a.key_room;
+    // Keys, and where the outputs are arrays of their own, every token's weight and
+    // position at its old place: the tokens that move are written after a barrier.
+    if (cut ? held || copies : copies) {
+#pragma unroll 4
+        for (int j = lo + tid; j < hi; j += kEvictThreads) {
+            const float w = a.weight[row + j];
+            const int p = a.pos[row + j];
+            if (cut && held) keys[j - lo] = evict_key(a, w, p, oldest_recent);
+            if (copies && j < a.budget) {
+                a.weight_out[row + j] = w;
+                a.pos_out[row + j] = p;
+            }
+        }
+    }
+    auto key = [&](int j) { return held ? keys[j - lo] : evict_key(a, a.weight[row + j], a.pos[row + j], oldest_recent); };
+    __syncthreads();
 
     // the largest key T with at least `budget` keys >= T; `above` keys are > T
-    uint32_t prefix = 0, mask = 0;
+    uint32_t T = 0, mask = 0;
     int above = 0;
     constexpr int shift_of[kDigits] = {21, 10, 0};
     constexpr int bits_of[kDigits] = {11, 11, 10};
-#pragma unroll
-    for (int d = 0; d < kDigits; ++d) {
-        const int shift = shift_of[d], bins = 1 << bits_of[d];
-        for (int i = tid; i < kHistBins; i += kSelectThreads) hist[i] = 0;
-        __syncthreads();
-        for (int j0 = 0; j0 < n; j0 += kSelectThreads) {
+#pragma unroll 1
+    for (int d = 0; cut && d < kDigits; ++d) {
+        const int shift = d == 0 ? shift_of[0] : d == 1 ? shift_of[1] : shift_of[2], bins = 1 << (d == 2 ? bits_of[2] : 11);
+        int* hist = sh.hist[d];
+        for (int j0 = lo; j0 < hi; j0 += kEvictThreads) {
             const int j = j0 + tid;
-            const uint32_t x = j < n ? key(j) : 0;
-            const bool in = j < n && (x & mask) == prefix;
+            const uint32_t x = j < hi ? key(j) : 0;
+            const bool in = j < hi && (x & mask) == T;
             const int bin = (x >> shift) & (bins - 1);
             // a warp whose tokens all fall into one bin adds once
             const uint32_t live = __ballot_sync(0xffffffffu, in);
@@ -171,110 +246,116 @@ __global__ void __launch_bounds__(kSelectThreads) kv_evict_select_kernel(const E
                 atomicAdd(&hist[bin], 1);
             }
         }
-        __syncthreads();
-        // thread t owns bins 2t and 2t + 1, counted from the top
-        const int hi = hist[kHistBins - 1 - 2 * tid], lo = hist[kHistBins - 2 - 2 * tid];
-        int incl = hi + lo;
+        sync();
+        // thread t adds up bins 2 t and 2 t + 1, counted from the top
+        const int top = kHistBins - 1 - 2 * tid;
+        int2 part[kEvictMaxCluster];
+#pragma unroll
+        for (int q = 0; q < kEvictMaxCluster; ++q)   // all asked for before the first is added
+            part[q] = q < ctas ? ld_cluster2(&hist[top - 1], q) : make_int2(0, 0);
+        int hi_bin = 0, lo_bin = 0;
+#pragma unroll
+        for (int q = 0; q < kEvictMaxCluster; ++q) {
+            hi_bin += part[q].y;
+            lo_bin += part[q].x;
+        }
+        int incl = hi_bin + lo_bin;
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
             const int o = __shfl_up_sync(0xffffffffu, incl, off);
             if (lane >= off) incl += o;
         }
-        const int base = warps_before(__shfl_sync(0xffffffffu, incl, 31), warp_sums);
-        const int before_hi = above + base + incl - hi - lo, before_lo = before_hi + hi;
-        if (before_hi < a.budget && before_lo >= a.budget) { sh_digit = kHistBins - 1 - 2 * tid; sh_above = before_hi; }
-        if (before_lo < a.budget && before_lo + lo >= a.budget) { sh_digit = kHistBins - 2 - 2 * tid; sh_above = before_lo; }
+        const int before = above + warps_before(__shfl_sync(0xffffffffu, incl, 31), sh.warp_sums) + incl - hi_bin - lo_bin;
+        const int b_hi = before, b_lo = before + hi_bin;
+        if (b_hi < a.budget && b_hi + hi_bin >= a.budget) { sh.digit = top; sh.above = b_hi; }
+        if (b_lo < a.budget && b_lo + lo_bin >= a.budget) { sh.digit = top - 1; sh.above = b_lo; }
         __syncthreads();
-        prefix |= sh_digit << shift;
+        T |= sh.digit << shift;
         mask |= (uint32_t)(bins - 1) << shift;
-        above = sh_above;
+        above = sh.above;
         __syncthreads();
     }
-    const uint32_t T = prefix;
-    const int ties = a.budget - above;   // of the keys equal to T the first `ties` stay
+    if (rank == 0 && tid == 0 && atomicAdd(&a.heads_in[b], 1u) == (unsigned)a.c.n_kv_heads - 1) {
+        a.heads_in[b] = 0;
+        a.lens_out[b] = min(n, a.budget);
+    }
+    if (!cut) {
+        sync();   // CTA 0's memory stays until its length has been read
+        return;
+    }
 
-    // each warp owns a contiguous range of tokens, so that ranks follow the index
-    const int span = (n + 32 * 32 - 1) / (32 * 32) * 32;
-    const int j_lo = warp * span, j_hi = min(n, j_lo + span);
-    int eq = 0;
-    for (int j = j_lo + lane; j < j_hi; j += 32) eq += key(j) == T;
-    eq = __reduce_add_sync(0xffffffffu, eq);
-    const int eq_base = warps_before(eq, warp_sums);
-    int holes = 0, moved = 0;
-    for (int pass = 0; pass < 2; ++pass) {   // counts, then places
-        int e = eq_base, hole_at = 0, move_at = 0;
-        if (pass == 1) {
-            hole_at = warps_before(holes, warp_sums);
-            move_at = warps_before(moved, warp_sums);
-        }
+    // Of the keys equal to T the first `ties` of the row stay.  A warp has a
+    // contiguous range of tokens and counts, below and past the budget, those above
+    // T and those at T; the places dropped and the tokens that move follow.
+    const int ties = a.budget - above;
+    const int wspan = (span / 32 + kEvictWarps - 1) / kEvictWarps * 32;
+    const int j_lo = min(hi, lo + warp * wspan), j_hi = min(hi, j_lo + wspan), j_cut = min(max(a.budget, j_lo), j_hi);
+    int above_in = 0, above_past = 0, at_in = 0, at_past = 0;
+    for (int j = j_lo + lane; j < j_hi; j += 32) {
+        const uint32_t x = key(j);
+        above_in += x > T && j < a.budget;
+        above_past += x > T && j >= a.budget;
+        at_in += x == T && j < a.budget;
+        at_past += x == T && j >= a.budget;
+    }
+    above_in = __reduce_add_sync(0xffffffffu, above_in);
+    above_past = __reduce_add_sync(0xffffffffu, above_past);
+    at_in = __reduce_add_sync(0xffffffffu, at_in);
+    at_past = __reduce_add_sync(0xffffffffu, at_past);
+    const int last_bin = (int)(T & ((1u << bits_of[2]) - 1));
+    int e = lane < rank ? ld_cluster(&sh.hist[2][last_bin], lane) : 0;
+    e = __reduce_add_sync(0xffffffffu, e) + warps_before(at_in + at_past, sh.warp_sums);
+    const int stay = min(max(ties - e, 0), at_in + at_past), stay_in = min(stay, at_in);
+    const int holes = j_cut - j_lo - above_in - stay_in, moved = above_past + stay - stay_in;
+    int hole_at = warps_before(holes, sh.warp_sums), move_at = warps_before(moved, sh.warp_sums);
+    if (warp == kEvictWarps - 1 && lane == 0) {
+        sh.holes = hole_at + holes;
+        sh.movers = move_at + moved;
+    }
+    sync();
+    const int all_holes = lane < ctas ? ld_cluster(&sh.holes, lane) : 0, all_moved = lane < ctas ? ld_cluster(&sh.movers, lane) : 0;
+    hole_at += __reduce_add_sync(0xffffffffu, lane < rank ? all_holes : 0);
+    move_at += __reduce_add_sync(0xffffffffu, lane < rank ? all_moved : 0);
+    const int total = __reduce_add_sync(0xffffffffu, all_moved);
+    int32_t* hole_list = a.holes + (int64_t)r * a.budget;
+    int32_t* move_list = a.movers + (int64_t)r * a.budget;
+    if (holes | moved)
         for (int j0 = j_lo; j0 < j_hi; j0 += 32) {
             const int j = j0 + lane;
             const uint32_t x = j < j_hi ? key(j) : 0;
-            const bool is_eq = j < j_hi && x == T;
-            const uint32_t before = (1u << lane) - 1;
-            const uint32_t eqs = __ballot_sync(0xffffffffu, is_eq);
-            const bool keep = j < j_hi && (x > T || (is_eq && e + __popc(eqs & before) < ties));
-            e += __popc(eqs);
+            const bool at = j < j_hi && x == T;
+            const uint32_t before = (1u << lane) - 1, ats = __ballot_sync(0xffffffffu, at);
+            const bool keep = j < j_hi && (x > T || (at && e + __popc(ats & before) < ties));
+            e += __popc(ats);
             const bool hole = j < j_hi && !keep && j < a.budget, mover = keep && j >= a.budget;
             const uint32_t hs = __ballot_sync(0xffffffffu, hole), ms = __ballot_sync(0xffffffffu, mover);
-            if (pass == 0) {
-                holes += __popc(hs);
-                moved += __popc(ms);
-            } else {
-                if (mover) movers[move_at + __popc(ms & before)] = j;
-                // a hole notes its rank (negative) until the movers are known
-                if (j < j_hi && j < a.budget) src[j] = hole ? -1 - (hole_at + __popc(hs & before)) : j;
-                hole_at += __popc(hs);
-                move_at += __popc(ms);
-            }
+            if (mover) move_list[move_at + __popc(ms & before)] = j;
+            if (hole) hole_list[hole_at + __popc(hs & before)] = j;
+            hole_at += __popc(hs);
+            move_at += __popc(ms);
         }
+    sync();   // the lists are written, and nobody reads this CTA's memory any more
+
+    if (a.moved) {   // the moves are another kernel's
+        if (rank == 0 && tid == 0) a.moved[r] = total;
+        return;
     }
-    __syncthreads();
-    for (int j = tid; j < a.budget; j += kSelectThreads) {
-        const int s = src[j];
-        if (s < 0) src[j] = movers[-1 - s];
-    }
+    const int share = (total + ctas - 1) / ctas, m_hi = min(total, (rank + 1) * share);
+    for (int m0 = rank * share; m0 < m_hi; m0 += kMovePairs)
+        move_pairs<LR, kEvictThreads>(a, b, h, row, hole_list + m0, move_list + m0, min(kMovePairs, m_hi - m0), sh.from, sh.to);
 }
 
-// One warp per 32 places of a row: their weights and positions, then the rows
-// of keys and values that move.  A token moves from an index >= budget to one
-// below it, so no place is both read and written and any order is right.
-template <int LR>   // lanes of a row: head_dim / 8
+// One CTA for kMovePairs pairs of a row's lists.
+constexpr int kMoveThreads = 256;
+template <int LR>
 __global__ void __launch_bounds__(kMoveThreads) kv_evict_move_kernel(const EvictArgs a) {
-    __shared__ int2 list[kMoveThreads / 32][32];
+    __shared__ int64_t from[kMovePairs], to[kMovePairs];
     griddep_wait();
-    const int r = blockIdx.y;
+    const int r = blockIdx.y, m0 = blockIdx.x * kMovePairs, count = min(kMovePairs, a.moved[r] - m0);
+    if (count <= 0) return;
     const int b = r / a.c.n_kv_heads, h = r % a.c.n_kv_heads;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int kept = a.kept[r];
-    if (blockIdx.x == 0 && h == 0 && threadIdx.x == 0) a.lens_out[b] = kept;
-    const int j = blockIdx.x * kMoveThreads + threadIdx.x;
-    int s = j;
-    if (j < kept) {
-        s = a.src[(int64_t)r * a.budget + j];
-        const int64_t row = b * a.track_seq + h * a.track_head;
-        const float w = a.weight[row + s];
-        const int p = a.pos[row + s];
-        a.weight_out[row + j] = w;
-        a.pos_out[row + j] = p;
-    }
-    const bool moves = j < kept && s != j;
-    const uint32_t ms = __ballot_sync(0xffffffffu, moves);
-    if (moves) list[warp][__popc(ms & ((1u << lane) - 1))] = make_int2(s, j);
-    __syncwarp();
-    const int items = 2 * __popc(ms);   // a key row and a value row for each move
-    constexpr int PER = 32 / LR;
-    const int piece = lane % LR;
-    for (int it = lane / LR; it < items; it += PER) {
-        const int2 m = list[warp][it >> 1];
-        const int64_t from = kv_offset(a.c, b, m.x), to = kv_offset(a.c, b, m.y);
-        if (from < 0 || to < 0) {
-            if (piece == 0) raise_status(a.status, MOE_W4_STATUS_BAD_INDEX);
-            continue;
-        }
-        uint16_t* base = const_cast<uint16_t*>(it & 1 ? a.c.v : a.c.k) + h * a.c.head_stride + piece * 8;
-        *reinterpret_cast<uint4*>(base + to) = *reinterpret_cast<const uint4*>(base + from);
-    }
+    const int64_t list = (int64_t)r * a.budget + m0;
+    move_pairs<LR, kMoveThreads>(a, b, h, b * a.track_seq + h * a.track_head, a.holes + list, a.movers + list, count, from, to);
 }
 
 static size_t evict_rows(const moe_w4_kv_cache& c) { return (size_t)c.n_seqs * c.n_kv_heads; }
@@ -283,6 +364,40 @@ static size_t evict_list_bytes(const moe_w4_kv_cache& c, int budget) {
 }
 static size_t evict_bytes(const moe_w4_kv_cache& c, int budget) {
     return MOE_W4_CTRL_BYTES + kSyncBytes + 2 * evict_list_bytes(c, budget) + round_up(evict_rows(c) * 4, 256);
+}
+
+template <int LR>
+static cudaError_t launch_evict(const EvictArgs& a, int rows, cudaStream_t st) {
+    static std::atomic<unsigned> ready;
+    int dev = 0;
+    if (sm_count(&dev) < 1) return cudaErrorInvalidDevice;
+    const cudaError_t e = allow_smem((const void*)kv_evict_kernel<LR>, kKeyRoom * 4, ready, dev);
+    if (e != cudaSuccess) return e;
+    // CTAs of a row: one up to 8192 tokens, where a barrier of a cluster costs more
+    // than it saves, then one per 4096, up to 8
+    int ctas = 1;
+    while (ctas < kEvictMaxCluster && a.max_len > 8192 && a.max_len > ctas * 4096) ctas *= 2;
+    EvictArgs b = a;
+    const int span = (int)((((int64_t)a.max_len + ctas - 1) / ctas + 31) & ~(int64_t)31);
+    b.key_room = span < kKeyRoom ? span : kKeyRoom;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = ctas;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)(rows * ctas));
+    cfg.blockDim = dim3(kEvictThreads);
+    cfg.dynamicSmemBytes = (size_t)b.key_room * 4;
+    cfg.stream = st;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    const cudaError_t e2 = cudaLaunchKernelEx(&cfg, kv_evict_kernel<LR>, b);
+    if (e2 != cudaSuccess || !b.moved) return e2;
+    const int most = a.budget < a.max_len - a.budget ? a.budget : a.max_len - a.budget;
+    return launch_pdl(true, kv_evict_move_kernel<LR>, dim3((unsigned)((most + kMovePairs - 1) / kMovePairs), (unsigned)rows),
+                      dim3(kMoveThreads), 0, st, b);
 }
 
 }  // namespace mw4
@@ -366,27 +481,18 @@ int moe_w4_kv_evict(const moe_w4_kv_cache* c, const moe_w4_kv_track* track, cons
     a.sink = sink;
     a.recent = recent;
     a.max_len = max_len;
-    a.key_room = max_len < kKeyRoom ? max_len : kKeyRoom;
-    a.chunks = c->head_dim / 8;
     uint8_t* ws = static_cast<uint8_t*>(workspace);
-    const size_t list = evict_list_bytes(*c, places);
-    a.src = reinterpret_cast<int32_t*>(ws + MOE_W4_CTRL_BYTES + kSyncBytes);
-    a.movers = reinterpret_cast<int32_t*>(ws + MOE_W4_CTRL_BYTES + kSyncBytes + list);
-    a.kept = reinterpret_cast<int32_t*>(ws + MOE_W4_CTRL_BYTES + kSyncBytes + 2 * list);
+    a.heads_in = reinterpret_cast<unsigned int*>(ws + MOE_W4_CTRL_BYTES + kRowSyncBytes);
+    a.holes = reinterpret_cast<int32_t*>(ws + MOE_W4_CTRL_BYTES + kSyncBytes);
+    a.movers = reinterpret_cast<int32_t*>(ws + MOE_W4_CTRL_BYTES + kSyncBytes + evict_list_bytes(*c, places));
     a.status = reinterpret_cast<unsigned int*>(ws);
-    const size_t smem = (size_t)a.key_room * 4;
-    static std::atomic<unsigned> ready;
-    int dev = 0;
-    if (sm_count(&dev) < 1) return MOE_W4_ERR_LAUNCH;
-    cudaError_t e = allow_smem((const void*)kv_evict_select_kernel, kKeyRoom * 4, ready, dev);
-    if (e == cudaSuccess)
-        e = launch_pdl(true, kv_evict_select_kernel, dim3((unsigned)rows), dim3(kSelectThreads), smem, stream, a);
-    if (e == cudaSuccess) {
-        auto kern = c->head_dim == 64 ? kv_evict_move_kernel<8>
-                    : c->head_dim == 128 ? kv_evict_move_kernel<16> : kv_evict_move_kernel<32>;
-        e = launch_pdl(true, kern, dim3((unsigned)((places + kMoveThreads - 1) / kMoveThreads), (unsigned)rows),
-                       dim3(kMoveThreads), 0, stream, a);
-    }
+    // Many moves want every SM: a kernel of their own.  Few are done by the CTAs
+    // that selected them, which saves its start.
+    const int64_t most = places < max_len - places ? places : max_len - places;
+    if (most * (int64_t)rows * c->head_dim * 8 > kInlineMoveBytes)
+        a.moved = reinterpret_cast<int32_t*>(ws + MOE_W4_CTRL_BYTES + kSyncBytes + 2 * evict_list_bytes(*c, places));
+    const cudaError_t e = c->head_dim == 64 ? launch_evict<8>(a, (int)rows, stream)
+                          : c->head_dim == 128 ? launch_evict<16>(a, (int)rows, stream) : launch_evict<32>(a, (int)rows, stream);
     return launched(e);
 }
 

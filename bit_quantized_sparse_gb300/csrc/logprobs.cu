@@ -162,25 +162,6 @@ MW4_DEV V warp_merge(V a, V b) {
     return v;
 }
 
-MW4_DEV uint32_t cluster_rank() {
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-MW4_DEV uint32_t cluster_size() {
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
-    return r;
-}
-MW4_DEV void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-// Shared memory of CTA 0 of the cluster.
-MW4_DEV uint32_t at_rank0(const void* p) {
-    uint32_t a;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(a) : "r"(smem_u32(p)));
-    return a;
-}
 MW4_DEV void st_cluster(uint32_t a, uint64_t v) { asm volatile("st.shared::cluster.u64 [%0], %1;" :: "r"(a), "l"(v) : "memory"); }
 MW4_DEV void st_cluster(uint32_t a, float v) { asm volatile("st.shared::cluster.f32 [%0], %1;" :: "r"(a), "f"(v) : "memory"); }
 
@@ -487,8 +468,8 @@ __global__ void __launch_bounds__(NT, kLpPerSm / NT) token_logprobs_kernel(const
         if (warp == 0) {
             s = warp_join(lane < (NT / 32) ? sh.sums[lane] : Sums{-INFINITY, 0.f, 0.f});
             if (ctas > 1) {
-                st_cluster(at_rank0(&sh.part_words[turn][rank][lane]), word);
-                if (lane < 3) st_cluster(at_rank0(&sh.part_sums[turn][rank][lane]), lane == 0 ? s.m : lane == 1 ? s.Z : s.U);
+                st_cluster(at_rank(&sh.part_words[turn][rank][lane], 0), word);
+                if (lane < 3) st_cluster(at_rank(&sh.part_sums[turn][rank][lane], 0), lane == 0 ? s.m : lane == 1 ? s.Z : s.U);
             }
         }
         if (ctas > 1) cluster_sync();

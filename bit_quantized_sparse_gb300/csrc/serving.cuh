@@ -50,6 +50,35 @@ MW4_DEV float ex2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+MW4_DEV uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+MW4_DEV uint32_t cluster_size() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+    return r;
+}
+MW4_DEV void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// This place of shared memory in CTA `rank` of the cluster.
+MW4_DEV uint32_t at_rank(const void* p, int rank) {
+    uint32_t a;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+    return a;
+}
+MW4_DEV int ld_cluster(const int* p, int rank) {
+    int v;
+    asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(at_rank(p, rank)) : "memory");
+    return v;
+}
+MW4_DEV int2 ld_cluster2(const int* p, int rank) {
+    int2 v;
+    asm volatile("ld.shared::cluster.v2.s32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(at_rank(p, rank)) : "memory");
+    return v;
+}
 constexpr float kLn2 = 0.693147180559945309f, kLog2e = 1.44269504088896341f;
 
 inline bool misaligned(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) != 0; }
@@ -89,9 +118,10 @@ inline KvView kv_view(const moe_w4_kv_cache& c) {
             c.pages_per_seq, c.n_seqs, c.n_kv_heads};
 }
 
-// Bytes after the control header that hold the attention's arrival records; the
-// other operators keep off them, since they must be zero between calls.
-constexpr int kSyncBytes = 8192;
+// Bytes after the control header that have to be zero between calls, so that
+// operators can share a workspace: the attention's arrival records, and the
+// eviction's counter for each sequence.
+constexpr int kRowSyncBytes = 8192, kSyncBytes = kRowSyncBytes + MOE_W4_MAX_SEQS * 4;
 
 __host__ __device__ constexpr size_t round_up(size_t v, size_t to) { return (v + to - 1) / to * to; }
 
