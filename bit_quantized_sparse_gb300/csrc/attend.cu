@@ -360,7 +360,7 @@ __global__ void __launch_bounds__(kAttThreads, AttCfg<D>::ctas) attend_kernel(co
     // Offsets are in pieces of 16 bytes.  The block table is read one tile ahead of
     // the keys: behind a full queue of them that load takes microseconds.
     Place ld = at;                 // the tile loaded next
-    int left = (int)(end - place); // places from ld's tile on; none left: nothing more to load
+    bool more = true;              // to load
     int token = at.tile * kTile + warp * kSub + (lane & 15);   // of ld's tile, this lane's to look up
     int page = -1;                 // of token
     uint64_t head_off = 0;         // of ld's row
@@ -423,24 +423,26 @@ __global__ void __launch_bounds__(kAttThreads, AttCfg<D>::ctas) attend_kernel(co
     int next_page = -1;            // read ahead, of the tile after ld
     Place ahead = at;
     int ahead_token = token;
-    int ahead_left = left;
+    uint32_t ahead_place = place;
+    bool more_ahead = true;
     auto read_ahead = [&]() {
-        --ahead_left;
+        ++ahead_place;
         if (++ahead.tile == ahead.tiles) {
-            ahead_left -= kRowCost;
+            ahead_place += kRowCost;
             next_row(lens, n_seqs, rows, ahead);
             ahead_token = warp * kSub + (lane & 15);
         } else {
             ahead_token += kTile;
         }
-        if (ahead_left > 0) next_page = read_page(ahead, ahead_token);
+        more_ahead = ahead_place < end;
+        if (more_ahead) next_page = read_page(ahead, ahead_token);
     };
     uint32_t fill = ring_u;
     bool values = false;           // the next unit is one of values
     auto load_unit = [&]() {
-        if (left > 0) {
+        if (more) {
             load(fill, values ? a.v : a.k);
-            if (values && (left = ahead_left) > 0) {
+            if (values && (more = more_ahead)) {
                 if (ahead.row != ld.row || ahead.b != ld.b) head_off = head_of(ahead);
                 ld = ahead;
                 token = ahead_token;
@@ -590,8 +592,9 @@ __global__ void __launch_bounds__(kAttThreads, AttCfg<D>::ctas) attend_kernel(co
         first_place = (int)place;
         fresh = true;
     };
+    bool open = true;              // tiles are left
 #pragma unroll 1
-    for (int u = -S; u < 0 || place < end || (u & 1); ++u) {
+    for (int u = -S; open; ++u) {
         if (fresh && u >= 0) {
             start_row();
             fresh = false;
@@ -705,7 +708,8 @@ __global__ void __launch_bounds__(kAttThreads, AttCfg<D>::ctas) attend_kernel(co
         const bool row_ends = at.tile == at.tiles - 1;
         if (u >= 0 && (u & 1)) {
             place += row_ends ? 1 + kRowCost : 1;
-            if (row_ends || place >= end) finish_row(row_ends);
+            open = place < end;
+            if (row_ends || !open) finish_row(row_ends);
             else ++at.tile;
         }
         load_unit();
@@ -726,22 +730,42 @@ __global__ void __launch_bounds__(kAttThreads, AttCfg<D>::ctas) attend_kernel(co
 }
 
 // weight_out[t] = weight[t] + sum over the kv head's query heads of p_t, from
-// the scores that the attention left.
-constexpr int kWeightThreads = 256;
+// the scores that the attention left.  Four tokens a thread; everything is asked
+// for at once, before the length is known (the scores' rows are whole multiples
+// of 16 tokens).
+constexpr int kWeightThreads = 128, kWeightTokens = 4;
 __global__ void __launch_bounds__(kWeightThreads) attend_weight_kernel(const AttendArgs a) {
     griddep_wait();
     const int b = blockIdx.z, kvh = blockIdx.y;
-    const int t = blockIdx.x * kWeightThreads + threadIdx.x;
-    if (t >= checked_len(a, b)) return;
-    float w = 0.f;
-    const int64_t head0 = (int64_t)b * a.n_q_heads + kvh * a.group;
-    for (int h = 0; h < a.group; ++h) {
-        const float lse2 = a.lse2[head0 + h];
-        const float s = a.scores[(head0 + h) * a.score_stride + t];
-        w += lse2 == -INFINITY ? 0.f : ex2(s - lse2);
+    const int t = (blockIdx.x * kWeightThreads + threadIdx.x) * kWeightTokens;
+    if (t >= a.max_len) return;
+    const int n = checked_len(a, b);
+    const int64_t e = b * a.track_seq + kvh * a.track_head + t, head0 = (int64_t)b * a.n_q_heads + kvh * a.group;
+    float before[kWeightTokens], w[kWeightTokens] = {};
+#pragma unroll
+    for (int k = 0; k < kWeightTokens; ++k) before[k] = t + k < n ? a.weight[e + k] : 0.f;
+    const float* scores = a.scores + head0 * a.score_stride + t;
+    for (int h0 = 0; h0 < a.group; h0 += 8) {
+        float4 s[8];
+        float lse2[8];
+#pragma unroll
+        for (int h = 0; h < 8; ++h) {
+            const bool in = h0 + h < a.group;
+            s[h] = in ? *reinterpret_cast<const float4*>(scores + (h0 + h) * a.score_stride) : make_float4(0.f, 0.f, 0.f, 0.f);
+            lse2[h] = in ? a.lse2[head0 + h0 + h] : -INFINITY;
+        }
+#pragma unroll
+        for (int h = 0; h < 8; ++h)
+            if (lse2[h] != -INFINITY) {
+                w[0] += ex2(s[h].x - lse2[h]);
+                w[1] += ex2(s[h].y - lse2[h]);
+                w[2] += ex2(s[h].z - lse2[h]);
+                w[3] += ex2(s[h].w - lse2[h]);
+            }
     }
-    const int64_t e = b * a.track_seq + kvh * a.track_head + t;
-    a.weight_out[e] = a.weight[e] + w;
+#pragma unroll
+    for (int k = 0; k < kWeightTokens; ++k)
+        if (t + k < n) a.weight_out[e + k] = before[k] + w[k];
 }
 
 struct AttendWs {
@@ -809,7 +833,8 @@ static cudaError_t launch_attend(const AttendArgs& a, cudaStream_t st) {
     } while (e == cudaErrorCooperativeLaunchTooLarge && (cudaGetLastError(), ctas /= 2) > 0);
     if (e == cudaSuccess && a.scores && a.max_len > 0)
         e = launch_pdl(true, attend_weight_kernel,
-                       dim3((a.max_len + kWeightThreads - 1) / kWeightThreads, a.c.n_kv_heads, a.c.n_seqs),
+                       dim3((a.max_len + kWeightThreads * kWeightTokens - 1) / (kWeightThreads * kWeightTokens),
+                            a.c.n_kv_heads, a.c.n_seqs),
                        dim3(kWeightThreads), 0, st, a);
     return e;
 }

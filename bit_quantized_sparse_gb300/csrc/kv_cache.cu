@@ -30,6 +30,7 @@ constexpr int kAppendThreads = 256;
 // the key and of the value.
 __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const AppendArgs a) {
     griddep_wait();
+    griddep_launch_dependents();   // the attention that follows may start to launch
     const int64_t at = (int64_t)blockIdx.x * kAppendThreads + threadIdx.x;
     const int per_token = a.c.n_kv_heads * a.chunks;
     const int i = (int)(at / per_token);

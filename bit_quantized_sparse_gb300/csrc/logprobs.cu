@@ -15,11 +15,13 @@
 // U = sum e (x - m), and its largest logit.
 //
 // The top k of a part: the k-th largest of the threads' maxima is a lower bound
-// tau of the k-th largest logit, so only threads whose maximum reaches tau (k
-// of them, more with ties) read their vectors again, from L2, and list what
-// reaches it; the list, a few entries more than k, is sorted by warps.  Ties
-// at tau and NaN can make the list too long or too short: paths of their own
-// below, exact for every input.
+// tau of the k-th largest logit.  A thread keeps the maximum of each quarter of
+// its vectors, so only about k quarters have to be read again, from L2, all of
+// them together by the whole CTA (a thread after the other it took 11 us a row
+// for the top 20 of 49,999: each access waits behind the stream of loads); what
+// reaches tau is listed, and the list, a few entries more than k, is sorted by
+// warps.  Ties at tau and NaN can make the list too long or too short: paths of
+// their own below, exact for every input.
 #include "serving.cuh"
 
 namespace mw4 {
@@ -49,6 +51,8 @@ constexpr int kLpStages = 3;
 constexpr int kLpPerSm = 1024;                            // resident threads per SM
 constexpr int kLpList = 256;                              // candidates listed before the paths for ties
 constexpr int kLpMaxCluster = 8;
+constexpr int kLpQuarters = 4;                            // maxima that a thread keeps
+constexpr int kLpAgain = 4;                               // vectors that a thread re-reads at a time
 constexpr float kLpLazy = 5.5f;                           // growth of the maximum before a rescale
 
 template <typename T> struct Logit;
@@ -185,6 +189,8 @@ struct Part {
         scalar = rank == 0 && tid < rest ? (tid < head ? tid : tid + vecs * E) : -1;
         count = (v1 - v0) * E + (rank == 0 ? rest : 0);
     }
+    // stages, and thus vectors of a thread, of a quarter
+    MW4_DEV int quarter_chunks() const { return (chunks() + kLpQuarters - 1) / kLpQuarters; }
     MW4_DEV int chunks() const { return max(1, (v1 - v0 + (NT * kLpVecs) - 1) / (NT * kLpVecs)); }
     MW4_DEV const uint4* vec(int v) const { return reinterpret_cast<const uint4*>(row + head) + v; }
     MW4_DEV int index(int v) const { return head + v * Logit<T>::E; }
@@ -195,18 +201,21 @@ struct LpShared {
     float lane_max[NT / 32][32];
     uint64_t sorted[NT / 32][32];
     uint64_t list[kLpList];
-    uint64_t part_words[2][kLpMaxCluster][32];   // of the cluster's CTAs, in CTA 0; by turns
-    float part_sums[2][kLpMaxCluster][3];
+    float quarter_max[kLpQuarters][NT];
+    uint16_t hits[kLpQuarters * NT];             // quarter and thread of the vectors to read again
+    static constexpr int kCtas = NT == 256 ? kLpMaxCluster : 1;   // smaller CTAs come one to a row
+    uint64_t part_words[2][kCtas][32];           // of the cluster's CTAs, in CTA 0; by turns
+    float part_sums[2][kCtas][3];
     Sums sums[NT / 32];
     int warp_count[NT / 32];
-    int count;
+    int count, hit_count;
     float tau;
 };
 
 // The kk largest words of a part by kk rounds over it.  Only for parts whose
 // list is too long for another reason than ties, or short of kk because of NaN.
 template <typename T, int NT>
-MW4_DEV uint64_t top_by_rounds(const Part<T, NT>& p, int kk, LpShared<NT>& sh) {
+__device__ __noinline__ uint64_t top_by_rounds(const Part<T, NT>& p, int kk, LpShared<NT>& sh) {
     constexpr int E = Logit<T>::E;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     uint64_t last = ~0ull, mine = 0;
@@ -240,12 +249,12 @@ MW4_DEV uint64_t top_by_rounds(const Part<T, NT>& p, int kk, LpShared<NT>& sh) {
     return mine;
 }
 
-// Lists the logits of the part that are >= tau (> tau where strict).  The warp
-// reads the vectors of one thread after the other that has such a logit.
+// Lists the logits of the part that are >= tau (> tau where strict).  Called by
+// the whole CTA, which then has to meet before it reads the list.
 template <typename T, int NT>
-MW4_DEV void list_from(const Part<T, NT>& p, float thread_max, float scalar, float tau, bool strict, LpShared<NT>& sh) {
+__device__ __noinline__ void list_from(const Part<T, NT>& p, float scalar, float tau, bool strict, LpShared<NT>& sh) {
     constexpr int E = Logit<T>::E;
-    const int lane = threadIdx.x & 31;
+    const int tid = threadIdx.x;
     auto see = [&](float x, int i) {
         if (strict ? x > tau : x >= tau) {
             const int at = atomicAdd(&sh.count, 1);
@@ -253,18 +262,40 @@ MW4_DEV void list_from(const Part<T, NT>& p, float thread_max, float scalar, flo
         }
     };
     if (p.scalar >= 0) see(scalar, p.scalar);
-    for (uint32_t hits = __ballot_sync(0xffffffffu, strict ? thread_max > tau : thread_max >= tau); hits; hits &= hits - 1) {
-        const int owner = (int)(threadIdx.x & ~31u) + __ffs(hits) - 1;
-        for (int v = p.v0 + owner + lane * NT; v < p.v1; v += 32 * NT) {
-            float2 x[E / 2];
-            Logit<T>::split(*p.vec(v), x);
-            if (max_of(x) >= tau) {
 #pragma unroll
-                for (int j = 0; j < E / 2; ++j) {
-                    see(x[j].x, p.index(v) + 2 * j);
-                    see(x[j].y, p.index(v) + 2 * j + 1);
-                }
+    for (int q = 0; q < kLpQuarters; ++q)
+        if (sh.quarter_max[q][tid] >= tau) sh.hits[atomicAdd(&sh.hit_count, 1)] = (uint16_t)(q * NT + tid);
+    __syncthreads();
+    const int per = p.quarter_chunks() * kLpVecs;      // vectors of a thread in a quarter
+    const int all = sh.hit_count * per;
+    auto place = [&](int e) {                          // e-th of the vectors to read again
+        const int hit = e / per, h = sh.hits[hit];
+        return p.v0 + h % NT + (h / NT * per + e - hit * per) * NT;
+    };
+    for (int e0 = tid; e0 - tid < all; e0 += NT * kLpAgain) {
+        uint4 v[kLpAgain];
+        uint32_t there = 0, mask = 0;                  // logits that reach tau, by vector
+#pragma unroll
+        for (int k = 0; k < kLpAgain; ++k) {
+            const int e = e0 + k * NT, at = e < all ? place(e) : p.v1;
+            if (at < p.v1) {
+                v[k] = *p.vec(at);
+                there |= 1u << k;
             }
+        }
+#pragma unroll
+        for (int k = 0; k < kLpAgain; ++k)
+            if (there >> k & 1) {
+                float2 x[E / 2];
+                Logit<T>::split(v[k], x);
+#pragma unroll
+                for (int j = 0; j < E / 2; ++j)
+                    mask |= (uint32_t)(strict ? x[j].x > tau : x[j].x >= tau) << (k * E + 2 * j) |
+                            (uint32_t)(strict ? x[j].y > tau : x[j].y >= tau) << (k * E + 2 * j + 1);
+            }
+        for (; mask; mask &= mask - 1) {               // few: one copy of this code, from the cache
+            const int bit = __ffs(mask) - 1, i = p.index(place(e0 + bit / E * NT)) + bit % E;
+            see(Logit<T>::one(p.row + i), i);
         }
     }
 }
@@ -272,7 +303,7 @@ MW4_DEV void list_from(const Part<T, NT>& p, float thread_max, float scalar, flo
 // Adds to the list the `need` lowest-indexed logits of the body that equal tau
 // (fewer if there are not so many), and all such logits outside it (at most 14).
 template <typename T, int NT>
-MW4_DEV void list_ties(const Part<T, NT>& p, float tau, int need, LpShared<NT>& sh) {
+__device__ __noinline__ void list_ties(const Part<T, NT>& p, float tau, int need, LpShared<NT>& sh) {
     constexpr int E = Logit<T>::E;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     if (p.scalar >= 0) {
@@ -309,12 +340,13 @@ MW4_DEV void list_ties(const Part<T, NT>& p, float tau, int need, LpShared<NT>& 
     }
 }
 
-// The kk largest words of a part, in lanes 0.. of warp 0.
+// The kk largest words of a part, in lanes 0.. of warp 0.  Not inlined: its
+// registers would make the streaming loop spill (4096 x 49999 fp16: 104 us).
 template <typename T, int NT>
-MW4_DEV uint64_t part_top(const Part<T, NT>& p, float thread_max, float scalar, int kk, LpShared<NT>& sh) {
+__device__ __noinline__ uint64_t part_top(const Part<T, NT>& p, float thread_max, float scalar, int kk, LpShared<NT>& sh) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     sh.lane_max[warp][lane] = warp_sort(thread_max);
-    if (tid == 0) sh.count = 0;
+    if (tid == 0) sh.count = sh.hit_count = 0;
 #pragma unroll
     for (int half = NT / 64; half; half >>= 1) {
         __syncthreads();
@@ -326,14 +358,14 @@ MW4_DEV uint64_t part_top(const Part<T, NT>& p, float thread_max, float scalar, 
     }
     __syncthreads();
     const float tau = sh.tau;
-    list_from(p, thread_max, scalar, tau, false, sh);
+    list_from(p, scalar, tau, false, sh);
     __syncthreads();
     int c = sh.count;
     if (c > kLpList) {   // many ties at tau: what exceeds it, then the first of them
         __syncthreads();
-        if (tid == 0) sh.count = 0;
+        if (tid == 0) sh.count = sh.hit_count = 0;
         __syncthreads();
-        list_from(p, thread_max, scalar, tau, true, sh);
+        list_from(p, scalar, tau, true, sh);
         __syncthreads();
         c = sh.count;
         __syncthreads();
@@ -413,7 +445,9 @@ __global__ void __launch_bounds__(NT, kLpPerSm / NT) token_logprobs_kernel(const
             if ((unsigned)target < (unsigned)a.vocab) target_x = Logit<T>::one(p.row + target);
         }
         Sums s{-INFINITY, 0.f, 0.f};
-        float most = -INFINITY, limit = -INFINITY;
+        float mine = -INFINITY, limit = -INFINITY;     // mine: of the present quarter
+        int turns = p.quarter_chunks();
+        float* quarter = &sh.quarter_max[0][tid];
         float2 Z = make_float2(0.f, 0.f), U = Z, minus = Z;
         for (int rest = p.v1 - p.v0 - tid, chunks = p.chunks(); chunks; --chunks, rest -= (NT * kLpVecs)) {
             cp_async_wait<kLpStages - 2>();
@@ -425,7 +459,7 @@ __global__ void __launch_bounds__(NT, kLpPerSm / NT) token_logprobs_kernel(const
                 float2 x[E / 2];
                 Logit<T>::split(at[i * NT], x);
                 const float vm = max_of(x);
-                most = fmaxf(most, vm);
+                mine = fmaxf(mine, vm);
                 // The reference follows the maximum when that has outgrown it by more than
                 // kLpLazy, so that a rescale is rare; the sums stay far inside fp32's range.
                 if (vm > limit) {
@@ -449,7 +483,21 @@ __global__ void __launch_bounds__(NT, kLpPerSm / NT) token_logprobs_kernel(const
                 }
             }
             stage = stage == kLpStages - 1 ? 0 : stage + 1;
+            if (--turns == 0) {
+                *quarter = mine;
+                quarter += NT;
+                mine = -INFINITY;
+                turns = p.quarter_chunks();
+            }
         }
+        float most = -INFINITY;
+        while (quarter <= &sh.quarter_max[kLpQuarters - 1][tid]) {
+            *quarter = mine;
+            quarter += NT;
+            mine = -INFINITY;
+        }
+#pragma unroll
+        for (int q = 0; q < kLpQuarters; ++q) most = fmaxf(most, sh.quarter_max[q][tid]);
         s.Z = Z.x + Z.y;
         s.U = U.x + U.y;
         if (p.scalar >= 0) {
@@ -467,15 +515,15 @@ __global__ void __launch_bounds__(NT, kLpPerSm / NT) token_logprobs_kernel(const
         else __syncthreads();
         if (warp == 0) {
             s = warp_join(lane < (NT / 32) ? sh.sums[lane] : Sums{-INFINITY, 0.f, 0.f});
-            if (ctas > 1) {
+            if (NT == 256 && ctas > 1) {
                 st_cluster(at_rank(&sh.part_words[turn][rank][lane], 0), word);
                 if (lane < 3) st_cluster(at_rank(&sh.part_sums[turn][rank][lane], 0), lane == 0 ? s.m : lane == 1 ? s.Z : s.U);
             }
         }
-        if (ctas > 1) cluster_sync();
+        if (NT == 256 && ctas > 1) cluster_sync();
         else __syncthreads();
         if (rank == 0 && warp == 0) {
-            if (ctas > 1) {
+            if (NT == 256 && ctas > 1) {
                 const float* q = sh.part_sums[turn][lane < ctas ? lane : 0];
                 s = warp_join(lane < ctas ? Sums{q[0], q[1], q[2]} : Sums{-INFINITY, 0.f, 0.f});
                 if (a.top)
