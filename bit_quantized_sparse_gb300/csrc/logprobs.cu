@@ -47,7 +47,7 @@ MW4_DEV float key_logit(uint32_t k) {
 MW4_DEV uint64_t logit_word(float x, int i) { return ((uint64_t)logit_key(x) << 32) | (uint32_t)~i; }
 
 constexpr int kLpVecs = 3;                                // vectors of a thread in a stage
-constexpr int kLpStages = 3;
+constexpr int kLpStages = 2;
 constexpr int kLpPerSm = 1024;                            // resident threads per SM
 constexpr int kLpList = 256;                              // candidates listed before the paths for ties
 constexpr int kLpMaxCluster = 8;
@@ -430,7 +430,7 @@ __global__ void __launch_bounds__(NT, kLpPerSm / NT) token_logprobs_kernel(const
         cp_async_commit();
     };
 #pragma unroll
-    for (int i = 0; i < kLpStages - 1; ++i) load(i);
+    for (int i = 0; i < kLpStages; ++i) load(i);
 
     int stage = 0, turn = 0;
     for (int r = first; r < a.n; r += step, turn ^= 1) {
@@ -450,8 +450,7 @@ __global__ void __launch_bounds__(NT, kLpPerSm / NT) token_logprobs_kernel(const
         float* quarter = &sh.quarter_max[0][tid];
         float2 Z = make_float2(0.f, 0.f), U = Z, minus = Z;
         for (int rest = p.v1 - p.v0 - tid, chunks = p.chunks(); chunks; --chunks, rest -= (NT * kLpVecs)) {
-            cp_async_wait<kLpStages - 2>();
-            load(stage == 0 ? kLpStages - 1 : stage - 1);
+            cp_async_wait<kLpStages - 1>();
             const uint4* at = &ring[stage * (NT * kLpVecs) + tid];
 #pragma unroll
             for (int i = 0; i < kLpVecs; ++i) {
@@ -482,6 +481,7 @@ __global__ void __launch_bounds__(NT, kLpPerSm / NT) token_logprobs_kernel(const
                     U = fma2(e, y, U);
                 }
             }
+            load(stage);   // into the slots just read: nobody else reads them
             stage = stage == kLpStages - 1 ? 0 : stage + 1;
             if (--turns == 0) {
                 *quarter = mine;

@@ -514,14 +514,17 @@ def test_refusals_leave_no_work(torch, sv):
         sv.token_logprobs(torch.zeros(2, 9, device="cuda"), top=10)
 
 
-@pytest.mark.parametrize("rows", [200, 700])
-def test_logprobs_many_rows(torch, sv, rows):
-    """More rows than the grid has places: CTAs and clusters take several in turn."""
+@pytest.mark.parametrize("rows,vocab,top,dtype", [(200, 5003, 9, "bfloat16"), (700, 5003, 9, "bfloat16"), (700, 7, 7, "float32"),
+                                                  (2000, 1031, 32, "float16"), (3001, 257, 0, "bfloat16"), (950, 9001, 1, "float32")])
+def test_logprobs_many_rows(torch, sv, rows, vocab, top, dtype):
+    """More rows than the grid has places: CTAs take several in turn.  Some rows are odd: masked, equal, with NaN."""
     g = torch.Generator(device="cuda")
     g.manual_seed(rows)
-    x = (torch.randn(rows, 5003, device="cuda", generator=g) * 3).to(torch.bfloat16)
-    t = torch.randint(0, 5003, (rows,), device="cuda", generator=g).to(torch.int32)
-    check_logprobs(torch, sv, x, t, 9)
+    x = (torch.randn(rows, vocab, device="cuda", generator=g) * 3).to(getattr(torch, dtype))
+    x[5], x[6, 1:], x[7, 0], x[rows - 1, ::2] = 1.5, float("-inf"), float("nan"), float("-inf")
+    x[8], x[9, -1] = float("-inf"), float("inf")
+    t = torch.randint(0, vocab, (rows,), device="cuda", generator=g).to(torch.int32)
+    check_logprobs(torch, sv, x, t, top)
 
 
 def test_attention_wait_timeout_is_reported(torch, sv):
