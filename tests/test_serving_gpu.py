@@ -541,3 +541,41 @@ def test_attention_wait_timeout_is_reported(torch, sv):
     assert s.cache.status() == 1
     assert mw.moe_w4_workspace_init(ptr, size, stream) == 0
     assert torch.equal(sv.attend_decode(s.cache, q), good) and s.cache.status() == 0
+
+
+def test_example_decodes_with_all_operators(torch, sv):
+    """examples/decode_loop.py: the first step against a plain computation, the cache within its budget, no status, the
+    same tokens every time."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "decode_loop.py")
+    spec = importlib.util.spec_from_file_location("decode_loop", path)
+    ex = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(ex)
+    (tokens, logprob, entropy), dec = ex.generate(70, seqs=3, budget=24, page=8)
+    assert dec.cache.status() == 0 and dec.layer.status() == 0 and sv.logprobs_status() == 0
+    n = dec.lens.tolist()
+    assert n == [dec.length] * 3 and dec.length <= 32
+    assert torch.isfinite(logprob).all() and torch.isfinite(entropy).all() and torch.all(logprob <= 0)
+    held = dec.cache.pos[:, :, :n[0]]
+    for b in range(3):
+        for h in range(2):
+            p = sorted(held[b, h].tolist())
+            assert len(set(p)) == len(p) and p[:2] == [0, 1] and p[-6:] == list(range(64, 70))   # sinks, and the newest
+    # every step hands out one unit of weight per query head: what is left is at most that
+    assert torch.all(dec.cache.weight[:, :, :n[0]].sum(2) <= 70 * 4 * (1 + 1e-4))
+    (again, _, _), _ = ex.generate(70, seqs=3, budget=24, page=8)
+    assert torch.equal(tokens, again)
+    # one token: attention returns its value vectors
+    fresh = ex.Decoder(seqs=3)
+    first = torch.arange(3, dtype=torch.int32, device="cuda")
+    x = fresh.embed[first.long()]
+    v = (fresh._normed(x) @ fresh.qkv).view(3, -1, 64)[:, -2:]
+    x = x + v.repeat_interleave(4, 1).reshape(3, -1) @ fresh.proj
+    from bit_quantized_sparse_gb300 import moe_w4 as mw
+    x = x + mw.forward_decode(fresh.layer, fresh._normed(x).contiguous())
+    logits = (fresh._normed(x) @ fresh.unembed).float()
+    following, best = fresh.step(first)
+    assert torch.equal(following.long(), logits.argmax(1))
+    want = torch.log_softmax(logits, 1).amax(1)
+    assert torch.allclose(best.top_logprob[:, 0], want, atol=1e-4)
