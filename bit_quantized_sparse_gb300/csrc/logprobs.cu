@@ -264,15 +264,23 @@ __device__ __noinline__ void list_from(const Part<T, NT>& p, float scalar, float
     if (p.scalar >= 0) see(scalar, p.scalar);
 #pragma unroll
     for (int q = 0; q < kLpQuarters; ++q)
-        if (sh.quarter_max[q][tid] >= tau) sh.hits[atomicAdd(&sh.hit_count, 1)] = (uint16_t)(q * NT + tid);
+        if (strict ? sh.quarter_max[q][tid] > tau : sh.quarter_max[q][tid] >= tau)
+            sh.hits[atomicAdd(&sh.hit_count, 1)] = (uint16_t)(q * NT + tid);
     __syncthreads();
+    // Ties, as in a row that is masked with -inf but for a few logits: each of
+    // these quarters holds one to list, so that the list would be too long.
+    if (sh.hit_count > kLpList) {
+        if (tid == 0) sh.count = sh.hit_count;
+        return;
+    }
     const int per = p.quarter_chunks() * kLpVecs;      // vectors of a thread in a quarter
     const int all = sh.hit_count * per;
     auto place = [&](int e) {                          // e-th of the vectors to read again
         const int hit = e / per, h = sh.hits[hit];
         return p.v0 + h % NT + (h / NT * per + e - hit * per) * NT;
     };
-    for (int e0 = tid; e0 - tid < all; e0 += NT * kLpAgain) {
+    // (a list that has grown too long is not read)
+    for (int e0 = tid; e0 - tid < all && *(volatile int*)&sh.count <= kLpList; e0 += NT * kLpAgain) {
         uint4 v[kLpAgain];
         uint32_t there = 0, mask = 0;                  // logits that reach tau, by vector
 #pragma unroll
