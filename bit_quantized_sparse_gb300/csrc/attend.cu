@@ -263,7 +263,7 @@ MW4_DEV bool join_row(const AttendArgs& a, uint8_t* smem, int b, int row, int c0
         cp_async_wait<0>();
         __syncthreads();
         // a group of lanes for a column, its lanes taking turns at the parts
-        const int turns = cols >= 128 ? 1 : cols >= 64 ? 2 : cols >= 32 ? 4 : cols >= 16 ? 8 : cols >= 8 ? 16 : 32;
+        const int turns = cols > 64 ? 1 : cols > 32 ? 2 : cols > 16 ? 4 : cols > 8 ? 8 : cols > 4 ? 16 : 32;
         const int turn = tid & (turns - 1);
 #pragma unroll 1
         for (int e = tid / turns; e < cols + kAttThreads / turns; e += kAttThreads / turns) {
@@ -271,12 +271,12 @@ MW4_DEV bool join_row(const AttendArgs& a, uint8_t* smem, int b, int row, int c0
             const int mine = min(e, cols - 1), h = (lo + mine) / Q;
             const float2* of = reinterpret_cast<const float2*>(ml) + h - h0;   // the head's, 2 pairs apart
             float M = -INFINITY, L = 0.f;
-#pragma unroll 1
+#pragma unroll 4
             for (int i = turn; i < parts; i += turns) M = fmaxf(M, of[i * 2 * pairs].x);
 #pragma unroll 1
             for (int off = turns / 2; off; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
             float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 1
+#pragma unroll 4
             for (int i = turn; i < parts; i += turns) {
                 const float2 x = of[i * 2 * pairs];
                 const float4 p = part[i * cols + mine];
@@ -548,8 +548,10 @@ __global__ void __launch_bounds__(kAttThreads, AttCfg<D>::ctas) attend_kernel(co
                 }
             __syncthreads();
             const int quads = min(8, heads - n * 8) * (D / 4);
-#pragma unroll 1
-            for (int e = threadIdx.x; e < quads; e += kAttThreads) {
+#pragma unroll
+            for (int i = 0; i < D / 64; ++i) {
+                const int e = threadIdx.x + i * kAttThreads;
+                if (e >= quads) break;
                 const int h8 = e / (D / 4), col = (e % (D / 4)) * 4, h = n * 8 + h8;
                 float M = sh_m[0][h], L = 0.f;
 #pragma unroll
@@ -719,13 +721,14 @@ __global__ void __launch_bounds__(kAttThreads, AttCfg<D>::ctas) attend_kernel(co
     griddep_launch_dependents();
 
     // the rows shared with other CTAs
-    if (begun_first >= 0) {
-        const int c0 = sh.owner(begun_first), parts = sh.owner(begun_first + begun_tiles - 1) - c0 + 1;
-        if (!join_row<T, D>(a, smem, begun_b, begun_row, c0, parts, cta - c0)) return;
-    }
-    if (open_first >= 0) {
-        const int parts = sh.owner(open_first + open_tiles - 1) - cta + 1;
-        join_row<T, D>(a, smem, open_b, open_row, cta, parts, 0);
+#pragma unroll 1
+    for (int which = 0; which < 2; ++which) {
+        if (begun_first >= 0) {
+            const int c0 = sh.owner(begun_first), parts = sh.owner(begun_first + begun_tiles - 1) - c0 + 1;
+            if (!join_row<T, D>(a, smem, begun_b, begun_row, c0, parts, cta - c0)) return;
+        }
+        begun_first = open_first;
+        begun_tiles = open_tiles; begun_b = open_b; begun_row = open_row;
     }
 }
 
