@@ -122,8 +122,14 @@ MW4_DEV uint32_t transpose8(uint32_t v) {
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(v));
     return d;
 }
-MW4_DEV void cp_async_16_to(uint32_t dst, const void* src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" :: "r"(dst), "l"(src) : "memory");
+MW4_DEV void cp_async_16_to(uint32_t dst, const void* src, uint64_t policy) {
+    asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2;" :: "r"(dst), "l"(src), "l"(policy) : "memory");
+}
+// The cache is read once a call: it leaves L2 before what is used again.
+MW4_DEV uint64_t read_once() {
+    uint64_t p;
+    asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
+    return p;
 }
 // 16 bytes, or zeros where !there (the source is not read then).
 MW4_DEV void cp_async_16_or_zero(uint32_t dst, const void* src, bool there) {
@@ -394,6 +400,7 @@ __global__ void __launch_bounds__(kAttThreads, AttCfg<D>::ctas) attend_kernel(co
     uint32_t swizzle[TURN];        // of this lane's piece in the rows that it copies
 #pragma unroll
     for (int i = 0; i < TURN; ++i) swizzle[i] = row0 * ROW + ((piece ^ ((i * PER + row0) & 7)) << 4);
+    const uint64_t policy = read_once();
     const bool packed = a.slot_pieces == CH;   // a run's rows follow one another
     auto load = [&](uint32_t base, const uint4* pool) {
         if (run) {
@@ -403,11 +410,11 @@ __global__ void __launch_bounds__(kAttThreads, AttCfg<D>::ctas) attend_kernel(co
             for (int i = 0; i < TURN; ++i) to[i] = base + swizzle[i];
             if (packed) {
 #pragma unroll
-                for (int i = 0; i < STEPS; ++i) cp_async_16_to(to[i % TURN] + i * PER * ROW, p + i * PER * CH);
+                for (int i = 0; i < STEPS; ++i) cp_async_16_to(to[i % TURN] + i * PER * ROW, p + i * PER * CH, policy);
             } else {
                 const uint32_t step = PER * a.slot_pieces;
 #pragma unroll
-                for (int i = 0; i < STEPS; ++i) cp_async_16_to(to[i % TURN] + i * PER * ROW, p + (uint64_t)i * step);
+                for (int i = 0; i < STEPS; ++i) cp_async_16_to(to[i % TURN] + i * PER * ROW, p + (uint64_t)i * step, policy);
             }
         } else if (any) {
 #pragma unroll 1
