@@ -106,11 +106,11 @@ constexpr int kMovePairs = 64;                   // tokens moved at a time by a 
 
 struct EvictShared {
     int hist[kDigits][kHistBins];
+    int groups[kDigits][32]; // sums of 64 bins
     int64_t from[kMovePairs], to[kMovePairs];
     int warp_sums[kEvictWarps];
     int holes, movers;       // of this CTA
-    uint32_t digit;
-    int above, n;
+    int bin, above, in_bin, n;
 };
 
 // Sum over the warps before this one of the warps' values (uniform in a warp).
@@ -206,75 +206,116 @@ __global__ void __launch_bounds__(kEvictThreads) kv_evict_kernel(const EvictArgs
     const bool cut = n > a.budget;
     const int64_t oldest_recent = (int64_t)a.seen[b] - a.recent;
     const bool held = span <= a.key_room;
-    // Keys, and where the outputs are arrays of their own, every token's weight and
-    // position at its old place: the tokens that move are written after a barrier.
-    if (cut ? held || copies : copies) {
-#pragma unroll 4
-        for (int j = lo + tid; j < hi; j += kEvictThreads) {
-            const float w = a.weight[row + j];
-            const int p = a.pos[row + j];
-            if (cut && held) keys[j - lo] = evict_key(a, w, p, oldest_recent);
-            if (copies && j < a.budget) {
-                a.weight_out[row + j] = w;
-                a.pos_out[row + j] = p;
+    // the digit of a warp's keys where their higher bits are T's
+    uint32_t T = 0, mask = 0;
+    auto count = [&](int* hist, int shift, int bins, uint32_t x, bool in) {
+        in = in && (x & mask) == T;
+        const int bin = (x >> shift) & (bins - 1);
+        // a warp whose tokens all fall into one bin adds once
+        const uint32_t live = __ballot_sync(0xffffffffu, in);
+        if (!live) return;
+        const int first = __shfl_sync(0xffffffffu, bin, __ffs(live) - 1);
+        if (__all_sync(0xffffffffu, !in || bin == first)) {
+            if (lane == 0) atomicAdd(&hist[first], __popc(live));
+        } else if (in) {
+            atomicAdd(&hist[bin], 1);
+        }
+    };
+    // Keys, counted by their first digit, and where the outputs are arrays of their
+    // own, every token's weight and position at its old place: the tokens that move
+    // are written after a barrier.
+    if (cut || copies) {
+        for (int j0 = lo + tid; j0 - tid < hi; j0 += kEvictThreads * kEvictUnroll) {
+            float w[kEvictUnroll];
+            int p[kEvictUnroll];
+#pragma unroll
+            for (int k = 0; k < kEvictUnroll; ++k) {
+                const int j = j0 + k * kEvictThreads;
+                w[k] = j < hi ? a.weight[row + j] : 0.f;
+                p[k] = j < hi ? a.pos[row + j] : 0;
+            }
+#pragma unroll
+            for (int k = 0; k < kEvictUnroll; ++k) {
+                const int j = j0 + k * kEvictThreads;
+                if (cut) {
+                    const uint32_t x = evict_key(a, w[k], p[k], oldest_recent);
+                    if (held && j < hi) keys[j - lo] = x;
+                    count(sh.hist[0], 21, kHistBins, x, j < hi);
+                }
+                if (copies && j < hi && j < a.budget) {
+                    a.weight_out[row + j] = w[k];
+                    a.pos_out[row + j] = p[k];
+                }
             }
         }
     }
     auto key = [&](int j) { return held ? keys[j - lo] : evict_key(a, a.weight[row + j], a.pos[row + j], oldest_recent); };
-    __syncthreads();
 
-    // the largest key T with at least `budget` keys >= T; `above` keys are > T
-    uint32_t T = 0, mask = 0;
-    int above = 0;
-    constexpr int shift_of[kDigits] = {21, 10, 0};
-    constexpr int bits_of[kDigits] = {11, 11, 10};
+    // T, the leading digits of the budget-th largest key: `above` keys have larger
+    // ones, at least `budget` larger or the same.  It is done when exactly `budget`
+    // have, as they mostly do after two digits, or when T is the whole key (ties).
+    int above = 0, last = 0, last_bin = 0;
 #pragma unroll 1
-    for (int d = 0; cut && d < kDigits; ++d) {
-        const int shift = d == 0 ? shift_of[0] : d == 1 ? shift_of[1] : shift_of[2], bins = 1 << (d == 2 ? bits_of[2] : 11);
+    for (int d = 0; cut; ++d) {
+        const int shift = d == 0 ? 21 : d == 1 ? 10 : 0, bins = d == 2 ? 1024 : 2048;
         int* hist = sh.hist[d];
-        for (int j0 = lo; j0 < hi; j0 += kEvictThreads) {
-            const int j = j0 + tid;
-            const uint32_t x = j < hi ? key(j) : 0;
-            const bool in = j < hi && (x & mask) == T;
-            const int bin = (x >> shift) & (bins - 1);
-            // a warp whose tokens all fall into one bin adds once
-            const uint32_t live = __ballot_sync(0xffffffffu, in);
-            if (!live) continue;
-            const int first = __shfl_sync(0xffffffffu, bin, __ffs(live) - 1);
-            if (__all_sync(0xffffffffu, !in || bin == first)) {
-                if (lane == 0) atomicAdd(&hist[first], __popc(live));
-            } else if (in) {
-                atomicAdd(&hist[bin], 1);
+        if (d)
+            for (int j0 = lo; j0 < hi; j0 += kEvictThreads) {
+                const int j = j0 + tid;
+                count(hist, shift, bins, j < hi ? key(j) : 0, j < hi);
+            }
+        __syncthreads();
+        const int2 two = *reinterpret_cast<const int2*>(&hist[2 * tid]);
+        const int group = __reduce_add_sync(0xffffffffu, two.x + two.y);
+        if (lane == 0) sh.groups[d][warp] = group;
+        sync();
+        if (warp == 0) {
+            // the group of 64 bins with T's digit, counted from the top, then the bin:
+            // two short trips to the other CTAs instead of all of their bins
+            int at = 31, before = above;
+#pragma unroll
+            for (int level = 0; level < 2; ++level) {
+                int2 part[kEvictMaxCluster];
+#pragma unroll
+                for (int q = 0; q < kEvictMaxCluster; ++q) {   // all asked for before the first is added
+                    part[q] = make_int2(0, 0);
+                    if (q < ctas) {
+                        if (level == 0) part[q].y = ld_cluster(&sh.groups[d][31 - lane], q);
+                        else part[q] = ld_cluster2(&hist[at * 64 + 62 - 2 * lane], q);
+                    }
+                }
+                int y = 0, x = 0;   // this lane's group, or its two bins: y the higher one
+#pragma unroll
+                for (int q = 0; q < kEvictMaxCluster; ++q) {
+                    y += part[q].y;
+                    x += part[q].x;
+                }
+                int incl = y + x;
+#pragma unroll
+                for (int off = 1; off < 32; off <<= 1) {
+                    const int o = __shfl_up_sync(0xffffffffu, incl, off);
+                    if (lane >= off) incl += o;
+                }
+                const int mine = before + incl - y - x;   // keys above
+                const int hit = __ffs(__ballot_sync(0xffffffffu, before + incl >= a.budget)) - 1 & 31;
+                if (level == 0) {
+                    at = 31 - hit;
+                    before = __shfl_sync(0xffffffffu, mine, hit);
+                } else if (lane == hit) {
+                    const bool upper = mine + y >= a.budget;
+                    sh.bin = at * 64 + 63 - 2 * lane - (upper ? 0 : 1);
+                    sh.above = upper ? mine : mine + y;
+                    sh.in_bin = upper ? y : x;
+                }
             }
         }
-        sync();
-        // thread t adds up bins 2 t and 2 t + 1, counted from the top
-        const int top = kHistBins - 1 - 2 * tid;
-        int2 part[kEvictMaxCluster];
-#pragma unroll
-        for (int q = 0; q < kEvictMaxCluster; ++q)   // all asked for before the first is added
-            part[q] = q < ctas ? ld_cluster2(&hist[top - 1], q) : make_int2(0, 0);
-        int hi_bin = 0, lo_bin = 0;
-#pragma unroll
-        for (int q = 0; q < kEvictMaxCluster; ++q) {
-            hi_bin += part[q].y;
-            lo_bin += part[q].x;
-        }
-        int incl = hi_bin + lo_bin;
-#pragma unroll
-        for (int off = 1; off < 32; off <<= 1) {
-            const int o = __shfl_up_sync(0xffffffffu, incl, off);
-            if (lane >= off) incl += o;
-        }
-        const int before = above + warps_before(__shfl_sync(0xffffffffu, incl, 31), sh.warp_sums) + incl - hi_bin - lo_bin;
-        const int b_hi = before, b_lo = before + hi_bin;
-        if (b_hi < a.budget && b_hi + hi_bin >= a.budget) { sh.digit = top; sh.above = b_hi; }
-        if (b_lo < a.budget && b_lo + lo_bin >= a.budget) { sh.digit = top - 1; sh.above = b_lo; }
         __syncthreads();
-        T |= sh.digit << shift;
+        last = d;
+        last_bin = sh.bin;
+        T |= (uint32_t)last_bin << shift;
         mask |= (uint32_t)(bins - 1) << shift;
         above = sh.above;
-        __syncthreads();
+        if (d == kDigits - 1 || above + sh.in_bin == a.budget) break;
     }
     if (rank == 0 && tid == 0 && atomicAdd(&a.heads_in[b], 1u) == (unsigned)a.c.n_kv_heads - 1) {
         a.heads_in[b] = 0;
@@ -285,15 +326,15 @@ __global__ void __launch_bounds__(kEvictThreads) kv_evict_kernel(const EvictArgs
         return;
     }
 
-    // Of the keys equal to T the first `ties` of the row stay.  A warp has a
-    // contiguous range of tokens and counts, below and past the budget, those above
-    // T and those at T; the places dropped and the tokens that move follow.
+    // Of the keys at T the first `ties` of the row stay.  A warp has a contiguous
+    // range of tokens and counts, below and past the budget, those above T and those
+    // at T; the places dropped and the tokens that move follow.
     const int ties = a.budget - above;
     const int wspan = (span / 32 + kEvictWarps - 1) / kEvictWarps * 32;
     const int j_lo = min(hi, lo + warp * wspan), j_hi = min(hi, j_lo + wspan), j_cut = min(max(a.budget, j_lo), j_hi);
     int above_in = 0, above_past = 0, at_in = 0, at_past = 0;
     for (int j = j_lo + lane; j < j_hi; j += 32) {
-        const uint32_t x = key(j);
+        const uint32_t x = key(j) & mask;
         above_in += x > T && j < a.budget;
         above_past += x > T && j >= a.budget;
         at_in += x == T && j < a.budget;
@@ -303,8 +344,7 @@ __global__ void __launch_bounds__(kEvictThreads) kv_evict_kernel(const EvictArgs
     above_past = __reduce_add_sync(0xffffffffu, above_past);
     at_in = __reduce_add_sync(0xffffffffu, at_in);
     at_past = __reduce_add_sync(0xffffffffu, at_past);
-    const int last_bin = (int)(T & ((1u << bits_of[2]) - 1));
-    int e = lane < rank ? ld_cluster(&sh.hist[2][last_bin], lane) : 0;
+    int e = lane < rank ? ld_cluster(&sh.hist[last][last_bin], lane) : 0;
     e = __reduce_add_sync(0xffffffffu, e) + warps_before(at_in + at_past, sh.warp_sums);
     const int stay = min(max(ties - e, 0), at_in + at_past), stay_in = min(stay, at_in);
     const int holes = j_cut - j_lo - above_in - stay_in, moved = above_past + stay - stay_in;
@@ -323,7 +363,7 @@ __global__ void __launch_bounds__(kEvictThreads) kv_evict_kernel(const EvictArgs
     if (holes | moved)
         for (int j0 = j_lo; j0 < j_hi; j0 += 32) {
             const int j = j0 + lane;
-            const uint32_t x = j < j_hi ? key(j) : 0;
+            const uint32_t x = j < j_hi ? key(j) & mask : 0;
             const bool at = j < j_hi && x == T;
             const uint32_t before = (1u << lane) - 1, ats = __ballot_sync(0xffffffffu, at);
             const bool keep = j < j_hi && (x > T || (at && e + __popc(ats & before) < ties));
