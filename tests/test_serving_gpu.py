@@ -357,6 +357,21 @@ def test_evict_long_rows(torch, sv):
     check_evict(torch, sv, s, s.lens.clone(), 20000, 4, 1000, False)
 
 
+def test_evict_row_that_shared_memory_cannot_hold(torch, sv):
+    s = Setup(torch, sv, [340001], 1, 64, 256, seed=18, track=True)
+    check_evict(torch, sv, s, s.lens.clone(), 90000, 4, 1000, False)
+
+
+@pytest.mark.parametrize("equal", [False, True])
+@pytest.mark.parametrize("budget,sink,recent", [(64, 4, 9), (257, 0, 0)])
+def test_evict_more_rows_than_sms(torch, sv, budget, sink, recent, equal):
+    lens = [(37 * b) % 531 for b in range(60)] + [2500, 1024]
+    s = Setup(torch, sv, lens, 4, 64, 16, seed=21, track=True)
+    if equal:
+        s.weight.fill_(0.5)
+    check_evict(torch, sv, s, s.lens + 3, budget, sink, recent, equal)
+
+
 def test_evict_more_protected_than_budget(torch, sv):
     """Positions that repeat can protect more tokens than fit: the first of them stay, still `budget` tokens."""
     s = Setup(torch, sv, [200], 1, 64, 16, seed=17, track=True)
