@@ -222,72 +222,108 @@ MW4_DEV void write_lse(const AttendArgs& a, int b, int head, float M, float L, b
     if (a.scores) a.lse2[at] = lse2;
 }
 
-// Adds up this CTA's share of the output of a row that `parts` CTAs have worked
-// on, c0 first; this is number `me` of them.  Returns false if a wait ran out.
+// A row that several CTAs have worked on, c0 first; none of them: parts = 0.
+struct Shared {
+    int c0, parts, b, row;
+};
+
+// Adds up this CTA's share of the outputs of the rows that it shares with others:
+// one begun before its part of the list and one going on after it, both at once,
+// as each step is a trip to L2 (64 sequences of up to 1000 tokens, 12 heads of 64,
+// one after the other: 17.9 us).
 template <typename T, int D>
-MW4_DEV bool join_row(const AttendArgs& a, uint8_t* smem, int b, int row, int c0, int parts, int me) {
-    __shared__ int sh_ok;
-    const int tid = threadIdx.x;
-    const int kvh = row / a.head_blocks, hb = row % a.head_blocks;
-    const int heads = min(kHeads, a.group - hb * kHeads), head0 = kvh * a.group + hb * kHeads;
-    __syncthreads();   // the ring and sh_ok are free
-    if (tid == 0) {
-        bool ok = true;
-        const uint64_t t0 = globaltimer();
-        for (int it = 0; ld_acquire(&a.sync[c0].arrived) < (unsigned)parts; ++it)
-            if ((it & 15) == 15 && globaltimer() - t0 > kWaitLimitNs) {
-                raise_status(&a.ctrl->status, MOE_W4_STATUS_WAIT_TIMEOUT);
-                ok = false;
-                break;
+MW4_DEV void join_rows(const AttendArgs& a, uint8_t* smem, int cta, const Shared& begun, const Shared& open) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    constexpr int Q = D / 4;                                  // columns of four outputs of a head
+    struct Share {                                            // of a row: its heads, this CTA's columns and their heads
+        int heads, head0, lo, cols, h0, pairs;
+    };
+    auto share = [&](const Shared& r) {
+        Share x{};
+        if (r.parts == 0) return x;
+        const int kvh = r.row / a.head_blocks, hb = r.row % a.head_blocks;
+        x.heads = min(kHeads, a.group - hb * kHeads);
+        x.head0 = kvh * a.group + hb * kHeads;
+        const int total = x.heads * Q, per = (total + r.parts - 1) / r.parts;
+        x.lo = (cta - r.c0) * per;
+        x.cols = max(0, min(per, total - x.lo));
+        x.h0 = x.lo / Q & ~1;
+        x.pairs = (x.lo + x.cols - 1) / Q / 2 - x.h0 / 2 + 1;
+        return x;
+    };
+    const Share xb = share(begun), xo = share(open);
+    bool ok = true;
+    if (lane == 0 && warp < 2) {
+        const int c0 = warp ? open.c0 : begun.c0;
+        const unsigned parts = warp ? open.parts : begun.parts;
+        if (parts) {
+            const uint64_t t0 = globaltimer();
+            for (int it = 0; ld_acquire(&a.sync[c0].arrived) < parts; ++it)
+                if ((it & 15) == 15 && globaltimer() - t0 > kWaitLimitNs) {
+                    raise_status(&a.ctrl->status, MOE_W4_STATUS_WAIT_TIMEOUT);
+                    ok = false;
+                    break;
+                }
+            // the last to have seen them all clears the row's record
+            if (ok && atomic_add_acq_rel_gpu(&a.sync[c0].left, 1) == parts - 1) {
+                a.sync[c0].arrived = 0;
+                a.sync[c0].left = 0;
             }
-        sh_ok = ok;
+        }
     }
-    __syncthreads();
-    if (!sh_ok) return false;
-    auto slot = [&](int i) { return (int64_t)((c0 + i) * 2 + (i == 0 ? 1 : 0)) * kHeads; };
-    // This CTA's columns of four outputs, and the heads that they belong to.
-    constexpr int Q = D / 4;                                  // columns of a head
-    const int total = heads * Q, per = (total + parts - 1) / parts;
-    const int lo = me * per, cols = min(per, total - lo);
-    if (cols > 0) {
-        // everything the sums need in one trip, a warp for a part in turn: the heads'
-        // maxima and sums (by pairs of heads), and the columns
-        const int h0 = lo / Q & ~1, pairs = (lo + cols - 1) / Q / 2 - h0 / 2 + 1;
-        float4* ml = reinterpret_cast<float4*>(smem);         // [parts][pairs]: m, sum, m, sum
-        float4* part = ml + parts * pairs;                    // [parts][cols]
-        const int lane = tid & 31, warp = tid >> 5;
+    if (!__syncthreads_and(ok)) return;                       // (the ring is free from here on)
+    // everything the sums need in one trip, a warp for a part in turn: the heads'
+    // maxima and sums (by pairs of heads), and the columns
+    float4* room = reinterpret_cast<float4*>(smem);           // [parts][pairs]: m, sum, m, sum; [parts][cols]; the next row's
+#pragma unroll 1
+    for (int which = 0; which < 2; ++which) {
+        const Shared r = which ? open : begun;
+        const Share x = which ? xo : xb;
+        if (x.cols == 0) continue;
+        float4* ml = room;
+        float4* part = ml + r.parts * x.pairs;
+        room = part + r.parts * x.cols;
         // few columns: several parts to a warp
-        const int wide = max(cols, pairs), lanes = wide >= 32 ? 32 : wide > 16 ? 32 : wide > 8 ? 16 : wide > 4 ? 8 : 4;
+        const int wide = max(x.cols, x.pairs), lanes = wide > 16 ? 32 : wide > 8 ? 16 : wide > 4 ? 8 : 4;
         const int sub = lane / lanes, in = lane & (lanes - 1), subs = 32 / lanes;
 #pragma unroll 1
-        for (int i = warp * subs + sub; i < parts; i += kAttWarps * subs) {
-            const int64_t sl = slot(i);
-            for (int e = in; e < pairs; e += lanes) cp_async_16(&ml[i * pairs + e], a.part_ml + (sl + h0 + e * 2) * 2);
-            for (int e = in; e < cols; e += lanes) cp_async_16(&part[i * cols + e], a.part_o + sl * D + (lo + e) * 4);
+        for (int i = warp * subs + sub; i < r.parts; i += kAttWarps * subs) {
+            const int64_t sl = (int64_t)((r.c0 + i) * 2 + (i == 0 ? 1 : 0)) * kHeads;
+            for (int e = in; e < x.pairs; e += lanes) cp_async_16(&ml[i * x.pairs + e], a.part_ml + (sl + x.h0 + e * 2) * 2);
+            for (int e = in; e < x.cols; e += lanes) cp_async_16(&part[i * x.cols + e], a.part_o + sl * D + (x.lo + e) * 4);
         }
-        cp_async_commit();
-        cp_async_wait<0>();
-        __syncthreads();
+    }
+    cp_async_commit();
+    cp_async_wait<0>();
+    __syncthreads();
+    room = reinterpret_cast<float4*>(smem);
+#pragma unroll 1
+    for (int which = 0; which < 2; ++which) {
+        const Shared r = which ? open : begun;
+        const Share x = which ? xo : xb;
+        if (x.cols == 0) continue;
+        const float4* ml = room;
+        const float4* part = ml + r.parts * x.pairs;
+        room += r.parts * (x.pairs + x.cols);
         // a group of lanes for a column, its lanes taking turns at the parts
-        const int turns = cols > 64 ? 1 : cols > 32 ? 2 : cols > 16 ? 4 : cols > 8 ? 8 : cols > 4 ? 16 : 32;
+        const int turns = x.cols > 64 ? 1 : x.cols > 32 ? 2 : x.cols > 16 ? 4 : x.cols > 8 ? 8 : x.cols > 4 ? 16 : 32;
         const int turn = tid & (turns - 1);
 #pragma unroll 1
-        for (int e = tid / turns; e < cols + kAttThreads / turns; e += kAttThreads / turns) {
-            if (e - tid / turns >= cols) break;   // the same for every lane
-            const int mine = min(e, cols - 1), h = (lo + mine) / Q;
-            const float2* of = reinterpret_cast<const float2*>(ml) + h - h0;   // the head's, 2 pairs apart
+        for (int e = tid / turns; e - tid / turns < x.cols; e += kAttThreads / turns) {   // the same turns for every lane
+            const int mine = min(e, x.cols - 1), h = (x.lo + mine) / Q;
+            const float2* of = reinterpret_cast<const float2*>(ml) + h - x.h0;   // the head's, 2 pairs apart
             float M = -INFINITY, L = 0.f;
 #pragma unroll 4
-            for (int i = turn; i < parts; i += turns) M = fmaxf(M, of[i * 2 * pairs].x);
+            for (int i = turn; i < r.parts; i += turns) M = fmaxf(M, of[i * 2 * x.pairs].x);
 #pragma unroll 1
             for (int off = turns / 2; off; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
             float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-            for (int i = turn; i < parts; i += turns) {
-                const float2 x = of[i * 2 * pairs];
-                const float4 p = part[i * cols + mine];
-                const float f = x.x == -INFINITY ? 0.f : ex2(x.x - M);
-                L += x.y * f;
+            for (int i = turn; i < r.parts; i += turns) {
+                const float2 y = of[i * 2 * x.pairs];
+                const float4 p = part[i * x.cols + mine];
+                const float f = y.x == -INFINITY ? 0.f : ex2(y.x - M);
+                L += y.y * f;
                 v.x += p.x * f; v.y += p.y * f; v.z += p.z * f; v.w += p.w * f;
             }
 #pragma unroll 1
@@ -298,23 +334,16 @@ MW4_DEV bool join_row(const AttendArgs& a, uint8_t* smem, int b, int row, int c0
                 v.z += __shfl_xor_sync(0xffffffffu, v.z, off);
                 v.w += __shfl_xor_sync(0xffffffffu, v.w, off);
             }
-            if (e < cols && turn == 0) {
+            if (e < x.cols && turn == 0) {
                 const bool none = M == -INFINITY && L == 0.f;
                 const float inv = none ? 0.f : 1.f / L;
-                const int col = (lo + e - h * Q) * 4;
-                *reinterpret_cast<uint2*>(a.out + b * a.out_stride + (int64_t)(head0 + h) * D + col) =
+                const int col = (x.lo + e - h * Q) * 4;
+                *reinterpret_cast<uint2*>(a.out + r.b * a.out_stride + (int64_t)(x.head0 + h) * D + col) =
                     make_uint2(Elem<T>::pack(v.x * inv, v.y * inv), Elem<T>::pack(v.z * inv, v.w * inv));
-                if (col == 0) write_lse(a, b, head0 + h, M, L, none);
+                if (col == 0) write_lse(a, r.b, x.head0 + h, M, L, none);
             }
         }
     }
-    if (tid == 0) {   // the last to leave clears the row's record
-        if (atomic_add_acq_rel_gpu(&a.sync[c0].left, 1) == (unsigned)parts - 1) {
-            a.sync[c0].arrived = 0;
-            a.sync[c0].left = 0;
-        }
-    }
-    return true;
 }
 
 // NB: blocks of 8 query heads of a row, 1 or 2.
@@ -728,15 +757,13 @@ __global__ void __launch_bounds__(kAttThreads, AttCfg<D>::ctas) attend_kernel(co
     griddep_launch_dependents();
 
     // the rows shared with other CTAs
-#pragma unroll 1
-    for (int which = 0; which < 2; ++which) {
-        if (begun_first >= 0) {
-            const int c0 = sh.owner(begun_first), parts = sh.owner(begun_first + begun_tiles - 1) - c0 + 1;
-            if (!join_row<T, D>(a, smem, begun_b, begun_row, c0, parts, cta - c0)) return;
-        }
-        begun_first = open_first;
-        begun_tiles = open_tiles; begun_b = open_b; begun_row = open_row;
+    Shared begun{0, 0, begun_b, begun_row}, going{(int)cta, 0, open_b, open_row};
+    if (begun_first >= 0) {
+        begun.c0 = sh.owner(begun_first);
+        begun.parts = sh.owner(begun_first + begun_tiles - 1) - begun.c0 + 1;
     }
+    if (open_first >= 0) going.parts = sh.owner(open_first + open_tiles - 1) - (int)cta + 1;
+    if (begun.parts | going.parts) join_rows<T, D>(a, smem, cta, begun, going);
 }
 
 // weight_out[t] = weight[t] + sum over the kv head's query heads of p_t, from
@@ -806,9 +833,9 @@ static cudaError_t launch_attend(const AttendArgs& a, cudaStream_t st) {
     const int sms = sm_count(&dev);
     if (sms < 1) return cudaErrorInvalidDevice;
     constexpr int ring = AttCfg<D>::slots * kAttWarps * unit_bytes(D);
-    // a join holds parts * cols < kHeads * D / 4 + parts columns, and parts * pairs <=
-    // kHeads / 2 + 2 parts maxima and sums
-    static_assert(ring >= 16 * (kHeads / 2 + 3 * most_ctas(D) + kHeads * D / 4), "a join fits the ring");
+    // the join of a row holds parts * cols < kHeads * D / 4 + parts columns, and parts *
+    // pairs <= kHeads / 2 + 2 parts maxima and sums; two rows share one CTA at most
+    static_assert(ring >= 16 * (kHeads + 3 * (most_ctas(D) + 1) + kHeads * D / 2), "a join fits the ring");
     static_assert(most_ctas(D) * sizeof(RowSync) <= kRowSyncBytes, "a record for every CTA");
     const int64_t rows = (int64_t)a.c.n_seqs * a.c.n_kv_heads * a.head_blocks;
     // no more CTAs than places that the longest lengths could make
