@@ -13,7 +13,7 @@ ready there.  Arguments are checked here (ValueError) and in the library
 leave out what is out of range and set the sticky status word
 (`PagedKVCache.status`, `logprobs_status`).  For use in a CUDA graph make one
 call of the same sizes on the capturing stream first, so that its workspace
-exists.
+exists; the cache keeps every workspace that a graph may hold.
 """
 from __future__ import annotations
 
@@ -116,7 +116,7 @@ class PagedKVCache:
             t.weight, t.pos, t.slots = weight.data_ptr(), mw._ptr(pos), weight.shape[2]
             t.seq_stride, t.head_stride = _stride(weight, 0), _stride(weight, 1)
             self._t = _byref(t)
-        self._ws, self._sizes = {}, {}
+        self._ws, self._sizes, self._kept = {}, {}, []
 
     @classmethod
     def allocate(cls, num_pages, page_size, n_kv_heads, head_dim, block_table, seq_lens, dtype=torch.bfloat16,
@@ -146,10 +146,14 @@ class PagedKVCache:
             raise ValueError("expected %s with the shape and strides of the cache's weights" % dtype)
 
     def _workspace(self, nbytes, stream, handle):
-        """(address, bytes) of the stream's workspace."""
+        """(address, bytes) of the stream's workspace.  One that has become too small is kept, as a CUDA graph may
+        hold its address; sizes double, so those kept are no more than the one in use."""
         ws = self._ws.get(handle)
         if ws is None or ws[1] < nbytes:
+            if ws is not None:
+                nbytes = max(nbytes, 2 * ws[1])
             t = _new_workspace(nbytes, self.device, stream)
+            self._kept.append(t)
             ws = self._ws[handle] = (t.data_ptr(), nbytes, t)
         return ws
 
@@ -157,8 +161,8 @@ class PagedKVCache:
         """The device status of the calls on this cache, all streams together (synchronises)."""
         torch.cuda.synchronize(self.device)
         got = 0
-        for ws in self._ws.values():
-            got |= _word(ws[2])
+        for ws in self._kept:
+            got |= _word(ws)
         return got
 
 

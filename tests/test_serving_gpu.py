@@ -224,6 +224,29 @@ def test_attention_is_deterministic_on_any_stream_and_in_graphs(torch, sv):
     assert torch.equal(out, sv.attend_decode(s.cache, q)) and not torch.equal(out[0], first[0][0])
 
 
+def test_graph_outlives_a_larger_workspace(torch, sv):
+    """A call that needs a larger workspace on the same stream leaves the one that a captured graph holds alone."""
+    s = Setup(torch, sv, [3000, 70], 2, 64, 16, seed=22, track=True)
+    q = s.randn(2, 8, 64).to(s.dt)
+    out, w = torch.empty_like(q), torch.zeros_like(s.weight)
+    good = sv.attend_decode(s.cache, q)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.stream(side):
+        sv.attend_decode(s.cache, q, out=out)
+        side.synchronize()
+        with torch.cuda.graph(graph, stream=side):
+            sv.attend_decode(s.cache, q, out=out)
+        sv.attend_decode(s.cache, q, weight_out=w)
+        waste = [torch.full((1 << 18,), -1, dtype=torch.int32, device="cuda") for _ in range(64)]   # takes what was freed
+    out.zero_()
+    torch.cuda.synchronize()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, good) and s.cache.status() == 0 and len(waste) == 64
+
+
 def test_attention_reports_bad_pages_and_lengths(torch, sv):
     """Pages outside the cache are left out, too long lengths are cut, and the status says so; the next cache is fine."""
     s = Setup(torch, sv, [100, 60], 1, 64, 16, seed=9)
