@@ -25,9 +25,15 @@
 //
 // Products are taken transposed, tokens (keys) or dimensions (values) as the 16
 // rows of an MMA and 8 query heads as its columns: S^T = K q^T, O^T = V^T P^T.
-// With queries as rows instead half of every product was empty at a group of
-// 8; 870 instructions per 16 tokens of 256 dimensions became about 300, and
-// issue latency, not HBM, had been the limit (131,072 tokens: 51 us).
+// With queries as rows instead half of every product was empty at a group of 8,
+// and issue, not HBM, was the limit.  Now a warp issues about 600 instructions
+// per 16 tokens of 256 dimensions, the tensor pipe is 11% busy, and loads are
+// what warps wait for.
+//
+// Measured (bf16, CUDA graph): 1 x 131,072 tokens, 2 kv heads of 256, group 8:
+// 47.8 us for 268 MB, 83% of the copy rate; 32 x 8192, 8 heads of 128, group 4:
+// 164 us for 1.07 GB, 96%.  A call's fixed cost is about 10 us: lengths and page
+// numbers (3 us), the first units (1.5), a row's end (2), its join (3).
 #include <climits>
 
 #include "serving.cuh"
@@ -42,8 +48,9 @@ constexpr int kHeads = 16;                      // query heads of a row, at most
 constexpr int kMaxSms = 160;                    // SMs that the workspace has room for
 constexpr float kLazyRescale = 8.f;             // log2 growth of the maximum before a rescale
 
-// Ring units per warp and CTAs per SM for a head size: about 190 KB of every SM
-// hold units in flight.
+// Ring units per warp and CTAs per SM for a head size: 130 to 175 KB of every SM
+// hold units in flight.  One more unit makes the queue longer, not the copies
+// faster (16 mixed sequences, heads of 128, 4 units: 80 us against 73 with 3).
 template <int D> struct AttCfg;
 template <> struct AttCfg<64> { static constexpr int slots = 5, ctas = 4; };
 template <> struct AttCfg<128> { static constexpr int slots = 3, ctas = 3; };
@@ -159,8 +166,8 @@ struct Shares {
 MW4_DEV int tiles_of(int len) { return max(1, (len + kTile - 1) / kTile); }
 // Places of a row in the list: its tiles and kRowCost more, with no tokens, for
 // what the end of a row costs, about the time of a tile.  Without them the CTAs
-// that got the short sequences of a mixed batch were the last by far (16
-// sequences of 1 to 32,768 tokens: 75 us).
+// that got the short sequences of a mixed batch are the last by far (16 sequences
+// of 1 to 32,768 tokens: 69.5 us against 64.0; with 2 the same 64.0).
 constexpr int kRowCost = 1;
 MW4_DEV uint32_t places_of(int len) { return tiles_of(len) + kRowCost; }
 

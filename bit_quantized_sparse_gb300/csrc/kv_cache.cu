@@ -27,7 +27,9 @@ struct AppendArgs {
 constexpr int kAppendThreads = 256;
 
 // One thread per 16-byte piece of a (token, head) row: it copies that piece of
-// the key and of the value.
+// the key and of the value.  Latency bounds it: one chain of three loads (index,
+// page number, data) and a store (16 tokens: 2.4 us, 4096 tokens of 2 heads of
+// 256: 3.8 us for 17 MB, 65% of the copy rate).
 __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const AppendArgs a) {
     griddep_wait();
     griddep_launch_dependents();   // the attention that follows may start to launch
@@ -67,8 +69,9 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const AppendA
 // ---------------------------------------------------------------------------
 // A row is a (sequence, head) and belongs to a cluster of 1 to 8 CTAs, each with
 // a contiguous range of its tokens:
-//   - the budget-th largest key T by three histogram passes over the key's
-//     digits, the CTAs' histograms added up through distributed shared memory;
+//   - the budget-th largest key T by two or three histogram passes over the
+//     key's digits, the CTAs' histograms added up through distributed shared
+//     memory;
 //   - which tokens stay (ties at T by index, ranks from the CTAs before), and
 //     two lists in ascending order: places below the budget that are dropped,
 //     tokens past it that are kept (as many);
@@ -76,8 +79,10 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const AppendA
 //     position of the token move into the place.
 // A token moves from an index >= budget to one below it, so no place is both
 // read and written and any order is right.
-// Bytes bound it in principle (keys read once, moved rows read and written);
-// at these sizes the chain of cluster barriers does.
+// Bytes bound it in principle (weights read once, moved rows read and written);
+// the chain of barriers does where few tokens move: 16 sequences of 4112 tokens to
+// 4096, 2 heads: 11.0 us.  4 sequences of up to 32,768 to 8192, 8 heads of 128:
+// 25 us, of which the selection takes 14 and the moves 8.
 struct EvictArgs {
     KvView c;
     const float* weight;
@@ -105,7 +110,10 @@ constexpr int kKeyRoom = 40 * 1024;              // keys that a CTA holds in sha
 // (4112 to 4096 tokens: 12.0 us with 4, 11.0 with 5, 11.3 with 8).
 constexpr int kKeyUnroll = 5;
 constexpr int kEvictUnroll = 4;                  // row pieces in flight of a thread
-constexpr int64_t kInlineMoveBytes = 4 << 20;    // moved by the selecting CTAs, at most
+// Bytes that the selecting CTAs move at most (as many as the lengths allow); more
+// go to a kernel on every SM.  16 x 4112 to 4096: 11.0 us inline, 12.0 with the
+// kernel; 4 x 32768 to 8192: 39.8 inline, 24.7 with it.
+constexpr int64_t kInlineMoveBytes = 4 << 20;
 constexpr int kMovePairs = 64;                   // tokens moved at a time by a CTA
 
 struct alignas(16) EvictShared {
@@ -421,8 +429,9 @@ static cudaError_t launch_evict(const EvictArgs& a, int rows, cudaStream_t st) {
     int dev = 0;
     const int sms = sm_count(&dev);
     if (sms < 1) return cudaErrorInvalidDevice;
-    // CTAs of a row: one up to 8192 tokens, where a barrier of a cluster costs more
-    // than it saves, then one per 4096, up to 8
+    // CTAs of a row: one up to 8192 tokens, where the barriers of a cluster cost more
+    // than they save (16 x 4112 to 4096: 11.0 us, with two 12.7), then one per 4096,
+    // up to 8 (4 x 16384 to 8192: 22.9 us; one per 8192: 26.6; one alone: 31.4)
     int ctas = 1;
     while (ctas < kEvictMaxCluster && a.max_len > 8192 && a.max_len > ctas * 4096) ctas *= 2;
     // One CTA a row and more rows than SMs: smaller CTAs, four to an SM (512 rows of

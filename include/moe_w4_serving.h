@@ -9,13 +9,19 @@
  * MOE_W4_ERR_* code, nothing enqueued on an argument error, deterministic
  * results (identical inputs give identical bytes), graph-capturable calls.
  *
- * Workspace.  Every call takes a workspace, 256-byte aligned, whose first
- * MOE_W4_CTRL_BYTES are the control header of moe_w4.h: clear it once with
- * moe_w4_workspace_init; the int32 at moe_w4_status_offset() is the sticky
- * device status (MOE_W4_STATUS_BAD_INDEX here: a sequence, slot, page, length
- * or token index read from device memory was out of range; what it would have
- * touched is left out, nothing out of range is accessed).  A workspace serves
- * one stream at a time; different operators may share one.
+ * Workspace.  Every call takes a workspace, 256-byte aligned, that is cleared
+ * once, as a whole, with moe_w4_workspace_init.  Its first MOE_W4_CTRL_BYTES are
+ * the control header of moe_w4.h: the int32 at moe_w4_status_offset() is the
+ * sticky device status.
+ *   MOE_W4_STATUS_BAD_INDEX: a sequence, slot, page, length or token index read
+ *     from device memory was out of range; what it would have touched is left
+ *     out, nothing out of range is accessed.
+ *   MOE_W4_STATUS_WAIT_TIMEOUT: in moe_w4_attend_decode a wait for another CTA's
+ *     part of a sequence ran out (2 s), as when the lengths change while it
+ *     runs; its output is not valid.  Clear the workspace before its next use.
+ * The attention and the eviction keep counters behind the header that are zero
+ * between calls.  A workspace serves one stream at a time; the operators of this
+ * header may share one, but not with a call of moe_w4.h.
  */
 #ifndef MOE_W4_SERVING_H
 #define MOE_W4_SERVING_H
@@ -31,7 +37,7 @@ enum { MOE_W4_TYPE_BF16 = 0, MOE_W4_TYPE_FP16 = 1, MOE_W4_TYPE_FP32 = 2 };
 #define MOE_W4_CTRL_BYTES 256
 #define MOE_W4_MAX_SEQS 4096        /* sequences of one cache               */
 #define MOE_W4_MAX_TOP 32           /* alternatives of moe_w4_token_logprobs */
-#define MOE_W4_MAX_VOCAB (1 << 20)
+#define MOE_W4_MAX_VOCAB (1 << 20)  /* logits of a row                       */
 
 /* A paged key-value cache.  The keys of page p, head h, slot s (0 <= s <
  * page_size) start at k + p * page_stride + h * head_stride + s * slot_stride
@@ -88,6 +94,8 @@ int moe_w4_kv_append(const moe_w4_kv_cache* c, const moe_w4_kv_track* track, int
 /* Attention of one new token per sequence over its seq_lens[b] cached tokens:
  *   s_t = scale * q . k_t,  p = softmax(s),  out = sum_t p_t v_t,
  *   lse = log sum_t exp(s_t)
+ * CTAs that share a sequence wait for one another, with a limit, so the launch is
+ * cooperative; moe_w4_test_skip_publish on its workspace makes those waits run out.
  * Query heads h * group .. h * group + group - 1 (group = n_q_heads /
  * n_kv_heads, at most 128) share kv head h.  Scores, softmax and sums are
  * fp32; out is rounded once.
@@ -102,7 +110,8 @@ int moe_w4_kv_append(const moe_w4_kv_cache* c, const moe_w4_kv_track* track, int
  *          strides of track; may be track->weight).  track->pos is not used.
  * A sequence of length 0, or whose scores are all -inf, gives zeros and lse
  * -inf.  Cache slots past the length are not read as numbers: they may hold
- * anything, NaN included. */
+ * anything, NaN included.  MOE_W4_ERR_UNSUPPORTED where n_seqs * n_kv_heads *
+ * (tiles of 64 tokens up to max_len + 1) * (blocks of 16 query heads) passes 2^31. */
 size_t moe_w4_attend_workspace_size(const moe_w4_kv_cache* c, int n_q_heads, int max_len, int with_track);
 int moe_w4_attend_decode(const moe_w4_kv_cache* c, int n_q_heads, const void* q, int64_t q_stride, float scale,
                          int max_len, void* out, int64_t out_stride, float* lse, const moe_w4_kv_track* track,
@@ -121,7 +130,7 @@ int moe_w4_attend_decode(const moe_w4_kv_cache* c, int n_q_heads, const void* q,
  * The outputs may be the inputs (lens_out == seq_lens, weight_out ==
  * track->weight, pos_out == track->pos) or separate arrays.  1 <= budget,
  * sink, recent >= 0, sink + recent <= budget; max_len as above, <=
- * track->slots. */
+ * track->slots; n_seqs * n_kv_heads <= 65535. */
 size_t moe_w4_evict_workspace_size(const moe_w4_kv_cache* c, int budget, int max_len);
 int moe_w4_kv_evict(const moe_w4_kv_cache* c, const moe_w4_kv_track* track, const int32_t* seen, int budget, int sink,
                     int recent, int max_len, int32_t* lens_out, float* weight_out, int32_t* pos_out, void* workspace,
