@@ -581,8 +581,12 @@ static cudaError_t launch_logprobs(const LogprobArgs& a, int ctas, int clusters,
     return cudaLaunchKernelEx(&cfg, token_logprobs_kernel<T, NT>, a);
 }
 
-// Few rows: CTAs of 256 threads, as many (up to 8) to a row as fit on the SMs at
-// once and still have a vector for every thread.  More rows than that: CTAs of
+// Few rows: CTAs of 256 threads, as many (up to 8) to a row as take three quarters
+// of the SMs' places and still have a vector for every thread.  Clusters do not
+// fit into every place (148 of 4 CTAs into 608; the rest would wait for a second
+// turn) and spread unevenly when they nearly fill them: 152 x 131072 bf16 took
+// 22.2 us with 4 CTAs a row, 15.8 with 2; 64 rows 13.4 with 8, 11.4 with 4.  Up to
+// half instead: 200 rows 21.8 us against 19.2.  More rows than places: CTAs of
 // 128 threads with a row each, whose row ends are shorter and overlap better
 // (4096 x 49999 fp16: 82 us against 90; for 16 x 131072 bf16 it is the other way
 // round, 12.0 against 10.3).
@@ -597,7 +601,7 @@ static cudaError_t launch_logprobs(const LogprobArgs& a, cudaStream_t st) {
         return launch_logprobs<T, 128>(a, 1, a.n < most ? a.n : most, dev, st);
     }
     int ctas = 1;
-    while (ctas < kLpMaxCluster && a.n * ctas * 2 <= places && vecs >= 256 * ctas * 2) ctas *= 2;
+    while (ctas < kLpMaxCluster && a.n * ctas * 2 <= places / 4 * 3 && vecs >= 256 * ctas * 2) ctas *= 2;
     return launch_logprobs<T, 256>(a, ctas, a.n, dev, st);
 }
 
