@@ -82,7 +82,7 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const AppendA
 // Bytes bound it in principle (weights read once, moved rows read and written);
 // the chain of barriers does where few tokens move: 16 sequences of 4112 tokens to
 // 4096, 2 heads: 11.0 us.  4 sequences of up to 32,768 to 8192, 8 heads of 128:
-// 25 us, of which the selection takes 14 and the moves 8.
+// 28 us, of which the selection takes 17 and the moves 8.
 struct EvictArgs {
     KvView c;
     const float* weight;
@@ -101,6 +101,7 @@ struct EvictArgs {
 };
 
 constexpr int kEvictThreads = 1024, kEvictManyThreads = 256;
+constexpr int kEvictManyTokens = 6144;           // four CTAs' keys fit into an SM
 constexpr int kEvictMaxCluster = 8;
 constexpr int kDigits = 3;                       // 11 + 11 + 10 bits of the key
 constexpr int kHistBins = 2048;                  // two bins a thread
@@ -112,7 +113,7 @@ constexpr int kKeyUnroll = 5;
 constexpr int kEvictUnroll = 4;                  // row pieces in flight of a thread
 // Bytes that the selecting CTAs move at most (as many as the lengths allow); more
 // go to a kernel on every SM.  16 x 4112 to 4096: 11.0 us inline, 12.0 with the
-// kernel; 4 x 32768 to 8192: 39.8 inline, 24.7 with it.
+// kernel; 4 x 32768 to 8192 (8 CTAs a row): 39.8 inline, 24.7 with it.
 constexpr int64_t kInlineMoveBytes = 4 << 20;
 constexpr int kMovePairs = 64;                   // tokens moved at a time by a CTA
 
@@ -431,12 +432,18 @@ static cudaError_t launch_evict(const EvictArgs& a, int rows, cudaStream_t st) {
     if (sms < 1) return cudaErrorInvalidDevice;
     // CTAs of a row: one up to 8192 tokens, where the barriers of a cluster cost more
     // than they save (16 x 4112 to 4096: 11.0 us, with two 12.7), then one per 4096,
-    // up to 8 (4 x 16384 to 8192: 22.9 us; one per 8192: 26.6; one alone: 31.4)
+    // up to 8 (4 x 16384 to 8192: 22.9 us; one per 8192: 26.6; one alone: 31.4), as
+    // long as all are resident at once: 32 rows of 65,536 tokens took 38.7 us with 8
+    // a row, in turns, 19.9 with 4; 32 rows of 32,768 to 8192 70 and 53 (but 24.7 and
+    // 28.2 where only 8 of them have anything to cut).  Clusters of 8 do not reach
+    // every SM (16 rows: 24.4 us, with 4 a row 19.5).
     int ctas = 1;
-    while (ctas < kEvictMaxCluster && a.max_len > 8192 && a.max_len > ctas * 4096) ctas *= 2;
+    while (ctas < kEvictMaxCluster && a.max_len > 8192 && a.max_len > ctas * 4096 &&
+           rows * ctas * 2 <= (ctas * 2 < kEvictMaxCluster ? sms : sms / 4 * 3))
+        ctas *= 2;
     // One CTA a row and more rows than SMs: smaller CTAs, four to an SM (512 rows of
     // 1000 tokens to 500: 35.6 -> 19.9 us; of 4112 to 4096: 35.2 -> 20.8).
-    const bool many = ctas == 1 && rows > sms;
+    const bool many = ctas == 1 && rows > sms && a.max_len <= kEvictManyTokens;
     auto kern = many ? kv_evict_kernel<LR, kEvictManyThreads> : kv_evict_kernel<LR, kEvictThreads>;
     const cudaError_t e = allow_smem((const void*)kern, kKeyRoom * 4, ready[many], dev);
     if (e != cudaSuccess) return e;
