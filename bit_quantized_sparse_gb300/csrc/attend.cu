@@ -51,12 +51,16 @@ constexpr float kLazyRescale = 8.f;             // log2 growth of the maximum be
 // Ring units per warp and CTAs per SM for a head size: 130 to 175 KB of every SM
 // hold units in flight.  One more unit makes the queue longer, not the copies
 // faster (16 mixed sequences, heads of 128, 4 units: 80 us against 73 with 3).
-template <int D> struct AttCfg;
-template <> struct AttCfg<64> { static constexpr int slots = 5, ctas = 4; };
-template <> struct AttCfg<128> { static constexpr int slots = 3, ctas = 3; };
-template <> struct AttCfg<256> { static constexpr int slots = 2, ctas = 2; };
+// NB blocks of 8 query heads: two of them at 128 dimensions do not fit the
+// registers of three CTAs an SM (1 x 16384 tokens, 4 kv heads, group 16: 20.2 us
+// with three, 16.6 with two; 256 x 300, 8 kv heads: 75.8 and 79.7).
+template <int D, int NB> struct AttCfg;
+template <int NB> struct AttCfg<64, NB> { static constexpr int slots = 5, ctas = 4; };
+template <> struct AttCfg<128, 1> { static constexpr int slots = 3, ctas = 3; };
+template <> struct AttCfg<128, 2> { static constexpr int slots = 5, ctas = 2; };
+template <int NB> struct AttCfg<256, NB> { static constexpr int slots = 2, ctas = 2; };
 constexpr int unit_bytes(int dim) { return kSub * dim * 2 + 128; }   // 128 more for the pitch of a warp's outputs
-constexpr int most_ctas(int dim) { return kMaxSms * (dim == 64 ? AttCfg<64>::ctas : dim == 128 ? AttCfg<128>::ctas : AttCfg<256>::ctas); }
+constexpr int most_ctas(int dim) { return kMaxSms * (dim == 64 ? AttCfg<64, 1>::ctas : dim == 128 ? AttCfg<128, 1>::ctas : AttCfg<256, 1>::ctas); }
 
 // Arrivals at a split row, by the first of its CTAs: how many partial results
 // are there, and how many of the row's CTAs are done with them.  The last to
@@ -355,10 +359,10 @@ MW4_DEV void join_rows(const AttendArgs& a, uint8_t* smem, int cta, const Shared
 
 // NB: blocks of 8 query heads of a row, 1 or 2.
 template <typename T, int D, int NB>
-__global__ void __launch_bounds__(kAttThreads, AttCfg<D>::ctas) attend_kernel(const AttendArgs a) {
+__global__ void __launch_bounds__(kAttThreads, AttCfg<D, NB>::ctas) attend_kernel(const AttendArgs a) {
     extern __shared__ __align__(1024) uint8_t smem[];
     __shared__ float sh_m[kAttWarps][kHeads], sh_l[kAttWarps][kHeads];
-    constexpr int S = AttCfg<D>::slots;
+    constexpr int S = AttCfg<D, NB>::slots;
     constexpr int ROW = D * 2;                       // bytes of a token's keys
     constexpr int UNIT = unit_bytes(D);              // keys or values of 16 tokens
     constexpr int CH = D / 8;                        // 16-byte pieces of a row
@@ -834,12 +838,12 @@ static AttendWs attend_ws(const moe_w4_kv_cache& c, int n_q_heads, int max_len, 
     return w;
 }
 
-template <typename T, int D>
+template <typename T, int D, int NB>
 static cudaError_t launch_attend(const AttendArgs& a, cudaStream_t st) {
     int dev = 0;
     const int sms = sm_count(&dev);
     if (sms < 1) return cudaErrorInvalidDevice;
-    constexpr int ring = AttCfg<D>::slots * kAttWarps * unit_bytes(D);
+    constexpr int ring = AttCfg<D, NB>::slots * kAttWarps * unit_bytes(D);
     // the join of a row holds parts * cols < kHeads * D / 4 + parts columns, and parts *
     // pairs <= kHeads / 2 + 2 parts maxima and sums; two rows share one CTA at most
     static_assert(ring >= 16 * (kHeads + 3 * (most_ctas(D) + 1) + kHeads * D / 2), "a join fits the ring");
@@ -849,13 +853,13 @@ static cudaError_t launch_attend(const AttendArgs& a, cudaStream_t st) {
     const int64_t tiles = a.max_len > kTile ? (a.max_len + kTile - 1) / kTile : 1, most = rows * (tiles + kRowCost);
     // the lengths of very many sequences cost a CTA of an SM
     const int smem = ring + (int)round_up((size_t)a.c.n_seqs * 4, 16);
-    const int per_sm = (228 << 10) / (smem + 2304) < AttCfg<D>::ctas ? (228 << 10) / (smem + 2304) : AttCfg<D>::ctas;
+    const int per_sm = (228 << 10) / (smem + 2304) < AttCfg<D, NB>::ctas ? (228 << 10) / (smem + 2304) : AttCfg<D, NB>::ctas;
     int64_t ctas = (int64_t)sms * per_sm;
     if (ctas > most_ctas(D)) ctas = most_ctas(D);
     if (ctas > most) ctas = most;
-    static std::atomic<unsigned> ready[2];
-    auto kern = a.group <= 8 ? attend_kernel<T, D, 1> : attend_kernel<T, D, 2>;
-    cudaError_t e = allow_smem((const void*)kern, ring + MOE_W4_MAX_SEQS * 4, ready[a.group <= 8 ? 0 : 1], dev);
+    static std::atomic<unsigned> ready;
+    const auto kern = attend_kernel<T, D, NB>;
+    cudaError_t e = allow_smem((const void*)kern, ring + MOE_W4_MAX_SEQS * 4, ready, dev);
     if (e != cudaSuccess) return e;
     // Rows can be cut only where there are more tiles than rows; CTAs that share a
     // row wait for one another, so all must be resident.
@@ -885,7 +889,9 @@ static cudaError_t launch_attend(const AttendArgs& a, cudaStream_t st) {
 
 template <typename T>
 static cudaError_t launch_attend_dim(int dim, const AttendArgs& a, cudaStream_t st) {
-    return dim == 64 ? launch_attend<T, 64>(a, st) : dim == 128 ? launch_attend<T, 128>(a, st) : launch_attend<T, 256>(a, st);
+    if (a.group <= 8)
+        return dim == 64 ? launch_attend<T, 64, 1>(a, st) : dim == 128 ? launch_attend<T, 128, 1>(a, st) : launch_attend<T, 256, 1>(a, st);
+    return dim == 64 ? launch_attend<T, 64, 2>(a, st) : dim == 128 ? launch_attend<T, 128, 2>(a, st) : launch_attend<T, 256, 2>(a, st);
 }
 
 static int check_heads(const moe_w4_kv_cache& c, int n_q_heads, int max_len) {
