@@ -541,18 +541,19 @@ __global__ void __launch_bounds__(NT, kLpPerSm / NT) token_logprobs_kernel(const
             }
             // a NaN, +inf (x - m is NaN then), or nothing but -inf
             const bool none = s.m == -INFINITY || isnan(s.Z);
-            const float logZ = log2f(s.Z) * kLn2;
-            const float lse = none ? NAN : s.m + logZ;
+            const float logZ = none ? NAN : log2f(s.Z) * kLn2;
+            // less m first: m + log Z would be rounded at the size of the logits
+            auto logprob = [&](float x) { return (x - s.m) - logZ; };
             if (lane < a.top) {
                 a.top_index[(int64_t)r * a.top + lane] = (int)~(uint32_t)word;
-                a.top_logprob[(int64_t)r * a.top + lane] = key_logit((uint32_t)(word >> 32)) - lse;
+                a.top_logprob[(int64_t)r * a.top + lane] = logprob(key_logit((uint32_t)(word >> 32)));
             }
             if (lane == 0) {
-                if (a.entropy) a.entropy[r] = none ? NAN : logZ - s.U / s.Z * kLn2;
+                if (a.entropy) a.entropy[r] = logZ - s.U / s.Z * kLn2;
                 if (a.targets) {
                     const bool in = (unsigned)target < (unsigned)a.vocab;
                     if (!in && target != -1) raise_status(a.status, MOE_W4_STATUS_BAD_INDEX);
-                    a.logprob[r] = in ? target_x - lse : target == -1 ? 0.f : NAN;
+                    a.logprob[r] = in ? logprob(target_x) : target == -1 ? 0.f : NAN;
                 }
             }
         }
