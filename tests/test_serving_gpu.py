@@ -529,6 +529,27 @@ def test_logprobs_deterministic_and_in_graphs(torch, sv):
     assert all(torch.equal(p, q) for p, q in zip(first, got))
 
 
+def test_empty_batches_and_bounds(torch, sv):
+    """No sequences, no tokens, no rows, a bound of 0: nothing happens, or zeros and -inf."""
+    def ints(*shape):
+        return torch.zeros(shape, dtype=torch.int32, device="cuda")
+    c = sv.PagedKVCache.allocate(4, 16, 2, 64, ints(0, 4), ints(0), track=True)
+    q = torch.zeros((0, 4, 64), dtype=torch.bfloat16, device="cuda")
+    assert sv.attend_decode(c, q, weight_out=c.weight).shape == q.shape
+    sv.kv_append(c, q[:, :2], q[:, :2])
+    sv.kv_evict(c, ints(0), 5)
+    r = sv.token_logprobs(torch.zeros((0, 10), device="cuda"), ints(0), 3)
+    assert r.logprob.shape == (0,) and r.top_index.shape == (0, 3)
+    s = Setup(torch, sv, [0, 3], 2, 64, 16, seed=23, track=True)
+    q, w = s.randn(2, 4, 64).to(s.dt), s.weight.clone()
+    s.lens.zero_()
+    out, lse = sv.attend_decode(s.cache, q, return_lse=True, weight_out=w, max_len=0)
+    assert torch.all(out == 0) and torch.all(lse == float("-inf")) and torch.equal(w, s.weight)
+    sv.kv_append(s.cache, q[:, :2], q[:, :2])       # idle sequences
+    sv.kv_evict(s.cache, s.lens, 5, max_len=0)
+    assert s.cache.status() == 0 and s.lens.tolist() == [0, 0]
+
+
 def test_refusals_leave_no_work(torch, sv):
     from bit_quantized_sparse_gb300.moe_w4 import MoeW4Error
     s = Setup(torch, sv, [20, 20], 2, 64, 8, seed=19)
