@@ -9,7 +9,7 @@
 // FMAs would already bound it at a group of 8).  mma.sync is enough here: a
 // tcgen05 tile of 128 rows would be nearly empty at 1 to 16 query heads.
 //
-// Work split.  A row is a (sequence, kv head, block of up to 16 query heads);
+// Work split.  A row is a (sequence, kv head, block of up to 24 query heads);
 // its tokens are cut into tiles of 64.  The tiles of all rows, in order, form
 // one list that the CTAs of a resident grid share out in equal contiguous
 // parts, so mixed lengths balance without the host knowing them.  A row that
@@ -44,22 +44,23 @@ constexpr int kAttWarps = 4;
 constexpr int kAttThreads = kAttWarps * 32;
 constexpr int kSub = 16;                        // tokens of a warp's part of a tile
 constexpr int kTile = kSub * kAttWarps;
-constexpr int kHeads = 16;                      // query heads of a row, at most
+constexpr int most_heads(int dim) { return dim == 256 ? 16 : 24; }   // query heads of a row
 constexpr int kMaxSms = 160;                    // SMs that the workspace has room for
 constexpr float kLazyRescale = 8.f;             // log2 growth of the maximum before a rescale
 
 // Ring units per warp and CTAs per SM for a head size: 130 to 175 KB of every SM
 // hold units in flight.  One more unit makes the queue longer, not the copies
 // faster (16 mixed sequences, heads of 128, 4 units: 80 us against 73 with 3).
-// NB blocks of 8 query heads: two of them at 128 dimensions do not fit the
-// registers of three CTAs an SM (1 x 16384 tokens, 4 kv heads, group 16: 20.2 us
-// with three, 16.6 with two; 256 x 300, 8 kv heads: 75.8 and 79.7).
+// NB blocks of 8 query heads: fewer CTAs where their outputs take the registers.
 template <int D, int NB> struct AttCfg;
 template <int NB> struct AttCfg<64, NB> { static constexpr int slots = 5, ctas = 4; };
+template <> struct AttCfg<64, 3> { static constexpr int slots = 6, ctas = 3; };
 template <> struct AttCfg<128, 1> { static constexpr int slots = 3, ctas = 3; };
-template <> struct AttCfg<128, 2> { static constexpr int slots = 5, ctas = 2; };
+template <> struct AttCfg<128, 2> { static constexpr int slots = 3, ctas = 3; };
+template <> struct AttCfg<128, 3> { static constexpr int slots = 5, ctas = 2; };
 template <int NB> struct AttCfg<256, NB> { static constexpr int slots = 2, ctas = 2; };
 constexpr int unit_bytes(int dim) { return kSub * dim * 2 + 128; }   // 128 more for the pitch of a warp's outputs
+constexpr int q_bytes(int dim, int blocks) { return blocks > 1 ? blocks * 8 * dim * 2 : 0; }
 constexpr int most_ctas(int dim) { return kMaxSms * (dim == 64 ? AttCfg<64, 1>::ctas : dim == 128 ? AttCfg<128, 1>::ctas : AttCfg<256, 1>::ctas); }
 
 // Arrivals at a split row, by the first of its CTAs: how many partial results
@@ -78,11 +79,11 @@ struct AttendArgs {
     const uint4* k;     // the pools and their strides in pieces of 16 bytes
     const uint4* v;
     uint32_t page_pieces, head_pieces, slot_pieces;
-    int n_q_heads, group, head_blocks, max_len;
+    int n_q_heads, group, head_blocks, block_heads, max_len;   // a kv head's query heads in blocks
     int runs;           // pages of a multiple of 16 slots: 16 tokens are one run in memory
     float scale_log2;   // scale * log2(e)
-    float* part_o;      // [2 * CTAs][kHeads][D] unnormalised outputs
-    float* part_ml;     // [2 * CTAs][kHeads][2] running maximum (log2) and sum
+    float* part_o;      // [2 * CTAs][8 NB][D] unnormalised outputs
+    float* part_ml;     // [2 * CTAs][8 NB][2] running maximum (log2) and sum
     RowSync* sync;      // [CTAs]
     float* scores;      // [n_seqs][n_q_heads][score_stride] log2 scores, or NULL
     float* lse2;        // [n_seqs][n_q_heads] log2 of the sums, with scores
@@ -126,6 +127,9 @@ MW4_DEV void ldsm4(uint32_t (&r)[4], uint32_t addr) {
 MW4_DEV void ldsm4_t(uint32_t (&r)[4], uint32_t addr) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+MW4_DEV void ldsm2(uint32_t (&r)[2], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x2.shared.b16 {%0,%1}, [%2];" : "=r"(r[0]), "=r"(r[1]) : "r"(addr) : "memory");
 }
 // An 8 x 8 block of 16-bit values, two a lane, transposed.
 MW4_DEV uint32_t transpose8(uint32_t v) {
@@ -242,7 +246,7 @@ struct Shared {
 // one begun before its part of the list and one going on after it, both at once,
 // as each step is a trip to L2 (64 sequences of up to 1000 tokens, 12 heads of 64,
 // one after the other: 17.9 us).
-template <typename T, int D>
+template <typename T, int D, int HEADS>
 MW4_DEV void join_rows(const AttendArgs& a, uint8_t* smem, int cta, const Shared& begun, const Shared& open) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     constexpr int Q = D / 4;                                  // columns of four outputs of a head
@@ -253,8 +257,8 @@ MW4_DEV void join_rows(const AttendArgs& a, uint8_t* smem, int cta, const Shared
         Share x{};
         if (r.parts == 0) return x;
         const int kvh = r.row / a.head_blocks, hb = r.row % a.head_blocks;
-        x.heads = min(kHeads, a.group - hb * kHeads);
-        x.head0 = kvh * a.group + hb * kHeads;
+        x.heads = min(a.block_heads, a.group - hb * a.block_heads);
+        x.head0 = kvh * a.group + hb * a.block_heads;
         const int total = x.heads * Q, per = (total + r.parts - 1) / r.parts;
         x.lo = (cta - r.c0) * per;
         x.cols = max(0, min(per, total - x.lo));
@@ -299,7 +303,7 @@ MW4_DEV void join_rows(const AttendArgs& a, uint8_t* smem, int cta, const Shared
         const int sub = lane / lanes, in = lane & (lanes - 1), subs = 32 / lanes;
 #pragma unroll 1
         for (int i = warp * subs + sub; i < r.parts; i += kAttWarps * subs) {
-            const int64_t sl = (int64_t)((r.c0 + i) * 2 + (i == 0 ? 1 : 0)) * kHeads;
+            const int64_t sl = (int64_t)((r.c0 + i) * 2 + (i == 0 ? 1 : 0)) * HEADS;
             for (int e = in; e < x.pairs; e += lanes) cp_async_16(&ml[i * x.pairs + e], a.part_ml + (sl + x.h0 + e * 2) * 2);
             for (int e = in; e < x.cols; e += lanes) cp_async_16(&part[i * x.cols + e], a.part_o + sl * D + (x.lo + e) * 4);
         }
@@ -357,11 +361,17 @@ MW4_DEV void join_rows(const AttendArgs& a, uint8_t* smem, int cta, const Shared
     }
 }
 
-// NB: blocks of 8 query heads of a row, 1 or 2.
+// NB: blocks of 8 query heads of a row, up to 3 (2 at 256 dimensions), so that a
+// group of up to 24 reads its keys and values once.  The queries of one block stay
+// in registers; those of more, whose outputs take their place, in shared memory
+// (4 x 16384 tokens, 2 kv heads of 256, group 16: 43.3 us with them in registers
+// that spill, 30.8 so; 16 x 16384, 4 heads of 128, group 24: 164.6 in two blocks of
+// the list, 99.5 in one, 537 MB).
 template <typename T, int D, int NB>
 __global__ void __launch_bounds__(kAttThreads, AttCfg<D, NB>::ctas) attend_kernel(const AttendArgs a) {
     extern __shared__ __align__(1024) uint8_t smem[];
-    __shared__ float sh_m[kAttWarps][kHeads], sh_l[kAttWarps][kHeads];
+    constexpr int HEADS = 8 * NB;
+    __shared__ float sh_m[kAttWarps][HEADS], sh_l[kAttWarps][HEADS];
     constexpr int S = AttCfg<D, NB>::slots;
     constexpr int ROW = D * 2;                       // bytes of a token's keys
     constexpr int UNIT = unit_bytes(D);              // keys or values of 16 tokens
@@ -377,7 +387,8 @@ __global__ void __launch_bounds__(kAttThreads, AttCfg<D, NB>::ctas) attend_kerne
     // The lengths, read once: whatever happens to them meanwhile, this CTA's view
     // of the list is one, and its accesses stay in range.
     const int rows = a.c.n_kv_heads * a.head_blocks, n_seqs = a.c.n_seqs;
-    int* lens = reinterpret_cast<int*>(smem + kAttWarps * S * UNIT);
+    uint8_t* q_smem = smem + kAttWarps * S * UNIT;        // [HEADS][D], pieces of a head swizzled like a unit's
+    int* lens = reinterpret_cast<int*>(q_smem + q_bytes(D, NB));
     const uint32_t cta = blockIdx.x;
     for (int b = threadIdx.x; b < n_seqs; b += kAttThreads) {
         const int n = a.c.lens[b];
@@ -508,24 +519,44 @@ __global__ void __launch_bounds__(kAttThreads, AttCfg<D, NB>::ctas) attend_kerne
     read_ahead();
 
     // ---- the queries of a row, and its running results ----
-    uint32_t qf[NB][D / 16][2];
+    uint32_t qf[D / 16][2];
     float o[NB][D / 16][4], m[NB][2], l[NB][2];
+    constexpr int QN = (HEADS * CH + kAttThreads - 1) / kAttThreads;   // pieces of a thread
+    uint4 qp[QN];
     auto load_q = [&](const Place& p) {
         const int kvh = p.row / a.head_blocks, hb = p.row % a.head_blocks;
-        const int heads = min(kHeads, a.group - hb * kHeads);
-        const uint16_t* q = a.q + p.b * a.q_stride + (int64_t)(kvh * a.group + hb * kHeads + g) * D + 2 * t4;
-#pragma unroll
-        for (int n = 0; n < NB; ++n)
+        const int heads = min(a.block_heads, a.group - hb * a.block_heads);
+        const uint16_t* q = a.q + p.b * a.q_stride + (int64_t)(kvh * a.group + hb * a.block_heads) * D;
+        if (NB == 1) {
+            q += g * D + 2 * t4;
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk) {
-                const bool in = g + 8 * n < heads;
-                qf[n][kk][0] = in ? *reinterpret_cast<const uint32_t*>(q + n * 8 * D + kk * 16) : 0u;
-                qf[n][kk][1] = in ? *reinterpret_cast<const uint32_t*>(q + n * 8 * D + kk * 16 + 8) : 0u;
+                qf[kk][0] = g < heads ? *reinterpret_cast<const uint32_t*>(q + kk * 16) : 0u;
+                qf[kk][1] = g < heads ? *reinterpret_cast<const uint32_t*>(q + kk * 16 + 8) : 0u;
             }
+        } else {
+#pragma unroll
+            for (int i = 0; i < QN; ++i) {
+                const int e = threadIdx.x + i * kAttThreads;
+                qp[i] = e < heads * CH ? *reinterpret_cast<const uint4*>(q + e * 8) : make_uint4(0u, 0u, 0u, 0u);
+            }
+        }
+    };
+    auto store_q = [&]() {
+#pragma unroll
+        for (int i = 0; i < QN; ++i) {
+            const int e = threadIdx.x + i * kAttThreads, h = e / CH;
+            if (e < HEADS * CH) *reinterpret_cast<uint4*>(q_smem + h * ROW + (((e % CH) ^ (h & 7)) << 4)) = qp[i];
+        }
     };
     load_q(at);
+    if (NB > 1) {
+        store_q();
+        __syncthreads();
+    }
     look_up();
-    // lanes' places in a unit of keys (rows tokens) and of values (rows tokens, transposed)
+    // lanes' places in a unit of keys (rows tokens) and of values (rows tokens, transposed);
+    // those of values are also the queries' (rows heads)
     uint32_t k_lane[4], v_lane[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -540,6 +571,7 @@ __global__ void __launch_bounds__(kAttThreads, AttCfg<D, NB>::ctas) attend_kerne
     int begun_tiles = 0, begun_b = 0, begun_row = 0, open_tiles = 0, open_b = 0, open_row = 0;
     const bool silent = cta == 0 && a.ctrl->pad[kCtrlInjectWord];   // the failure-detection test hook
     uint32_t take = ring_u;        // the next unit to use
+    const uint32_t q_u = smem_u32(q_smem);
 
     // One turn a unit, the first S of them only to fill the ring: a single copy of
     // the loading code, as this kernel runs through much of its code just once.
@@ -550,8 +582,8 @@ __global__ void __launch_bounds__(kAttThreads, AttCfg<D, NB>::ctas) attend_kerne
     uint32_t hi[NB][2], lo[NB][2]; // P^T of tokens 0..7 and 8..15: 16 bits, and what they leave
     auto start_row = [&]() {
         const int kvh = at.row / a.head_blocks, hb = at.row - kvh * a.head_blocks;
-        heads = min(kHeads, a.group - hb * kHeads);
-        head0 = kvh * a.group + hb * kHeads;
+        heads = min(a.block_heads, a.group - hb * a.block_heads);
+        head0 = kvh * a.group + hb * a.block_heads;
         first = at.tile;
 #pragma unroll
         for (int n = 0; n < NB; ++n) {
@@ -568,7 +600,7 @@ __global__ void __launch_bounds__(kAttThreads, AttCfg<D, NB>::ctas) attend_kerne
     auto finish_row = [&](bool row_ends) {
         Place nx = at;
         next_row(lens, n_seqs, rows, nx);
-        if (place < end) load_q(nx);    // there by the time the next row begins
+        if (NB == 1 && place < end) load_q(nx);    // there by the time the next row begins
 #pragma unroll
         for (int n = 0; n < NB; ++n)
 #pragma unroll
@@ -581,7 +613,7 @@ __global__ void __launch_bounds__(kAttThreads, AttCfg<D, NB>::ctas) attend_kerne
                 }
             }
         const bool whole = row_ends && first == 0;
-        const int64_t slot = (int64_t)(cta * 2 + (first == 0 ? 1 : 0)) * kHeads;
+        const int64_t slot = (int64_t)(cta * 2 + (first == 0 ? 1 : 0)) * HEADS;
         const uint32_t here = take - ring_u;
         float* buf = reinterpret_cast<float*>(ring + here) + 2 * t4 * (D + 4) + g;   // [8][D + 4]: no bank twice
 #pragma unroll
@@ -594,6 +626,8 @@ __global__ void __launch_bounds__(kAttThreads, AttCfg<D, NB>::ctas) attend_kerne
                     buf[c * (D + 4) + j * 16 + 8] = o[n][j][c + 2];
                 }
             __syncthreads();
+            const bool next_q = NB > 1 && n == NB - 1 && place < end;   // nobody uses the present ones any more
+            if (next_q) load_q(nx);
             const int quads = min(8, heads - n * 8) * (D / 4);
 #pragma unroll
             for (int i = 0; i < D / 64; ++i) {
@@ -624,6 +658,7 @@ __global__ void __launch_bounds__(kAttThreads, AttCfg<D, NB>::ctas) attend_kerne
                     if (col == 0) __stcg(reinterpret_cast<float2*>(a.part_ml + (slot + h) * 2), make_float2(M, L));
                 }
             }
+            if (next_q) store_q();
             __syncthreads();
         }
         if (!whole) {
@@ -667,8 +702,19 @@ __global__ void __launch_bounds__(kAttThreads, AttCfg<D, NB>::ctas) attend_kerne
                 for (int kk = 0; kk < D / 16; ++kk) {
                     uint32_t k4[4];
                     ldsm4(k4, from[kk & 3] + (kk >> 2) * 128);
-#pragma unroll
-                    for (int n = 0; n < NB; ++n) Elem<T>::mma(s[n][kk & 1], k4, qf[n][kk][0], qf[n][kk][1]);
+                    if (NB == 1) {
+                        Elem<T>::mma(s[0][kk & 1], k4, qf[kk][0], qf[kk][1]);
+                    } else {
+                        uint32_t q4[4];
+                        ldsm4(q4, q_u + v_lane[kk & 3] + (kk >> 2) * 128);
+                        Elem<T>::mma(s[0][kk & 1], k4, q4[0], q4[1]);
+                        Elem<T>::mma(s[1 % NB][kk & 1], k4, q4[2], q4[3]);
+                        if (NB == 3) {
+                            uint32_t q2[2];
+                            ldsm2(q2, q_u + 16 * ROW + v_lane[kk & 3] + (kk >> 2) * 128);
+                            Elem<T>::mma(s[NB - 1][kk & 1], k4, q2[0], q2[1]);
+                        }
+                    }
                 }
             }
             {
@@ -774,7 +820,7 @@ __global__ void __launch_bounds__(kAttThreads, AttCfg<D, NB>::ctas) attend_kerne
         begun.parts = sh.owner(begun_first + begun_tiles - 1) - begun.c0 + 1;
     }
     if (open_first >= 0) going.parts = sh.owner(open_first + open_tiles - 1) - (int)cta + 1;
-    if (begun.parts | going.parts) join_rows<T, D>(a, smem, cta, begun, going);
+    if (begun.parts | going.parts) join_rows<T, D, HEADS>(a, smem, cta, begun, going);
 }
 
 // weight_out[t] = weight[t] + sum over the kv head's query heads of p_t, from
@@ -827,8 +873,8 @@ static AttendWs attend_ws(const moe_w4_kv_cache& c, int n_q_heads, int max_len, 
     size_t o = MOE_W4_CTRL_BYTES + kSyncBytes;
     auto take = [&](size_t bytes) { const size_t at = o; o += round_up(bytes, 256); return at; };
     w.sync = MOE_W4_CTRL_BYTES;
-    w.part_o = take((size_t)2 * most_ctas(c.head_dim) * kHeads * c.head_dim * 4);
-    w.part_ml = take((size_t)2 * most_ctas(c.head_dim) * kHeads * 2 * 4);
+    w.part_o = take((size_t)2 * most_ctas(c.head_dim) * most_heads(c.head_dim) * c.head_dim * 4);
+    w.part_ml = take((size_t)2 * most_ctas(c.head_dim) * most_heads(c.head_dim) * 2 * 4);
     w.score_stride = (int64_t)round_up((size_t)max_len, kSub);
     if (track) {
         w.lse2 = take((size_t)c.n_seqs * n_q_heads * 4);
@@ -844,22 +890,23 @@ static cudaError_t launch_attend(const AttendArgs& a, cudaStream_t st) {
     const int sms = sm_count(&dev);
     if (sms < 1) return cudaErrorInvalidDevice;
     constexpr int ring = AttCfg<D, NB>::slots * kAttWarps * unit_bytes(D);
-    // the join of a row holds parts * cols < kHeads * D / 4 + parts columns, and parts *
-    // pairs <= kHeads / 2 + 2 parts maxima and sums; two rows share one CTA at most
-    static_assert(ring >= 16 * (kHeads + 3 * (most_ctas(D) + 1) + kHeads * D / 2), "a join fits the ring");
+    // the join of a row holds parts * cols < 8 NB * D / 4 + parts columns, and parts *
+    // pairs <= 4 NB + 2 parts maxima and sums; two rows share one CTA at most
+    static_assert(ring >= 16 * (8 * NB + 3 * (kMaxSms * AttCfg<D, NB>::ctas + 1) + 4 * NB * D), "a join fits the ring");
+    static_assert(AttCfg<D, NB>::ctas * kMaxSms <= most_ctas(D), "the workspace holds every CTA's parts");
     static_assert(most_ctas(D) * sizeof(RowSync) <= kRowSyncBytes, "a record for every CTA");
     const int64_t rows = (int64_t)a.c.n_seqs * a.c.n_kv_heads * a.head_blocks;
     // no more CTAs than places that the longest lengths could make
     const int64_t tiles = a.max_len > kTile ? (a.max_len + kTile - 1) / kTile : 1, most = rows * (tiles + kRowCost);
     // the lengths of very many sequences cost a CTA of an SM
-    const int smem = ring + (int)round_up((size_t)a.c.n_seqs * 4, 16);
+    const int smem = ring + q_bytes(D, NB) + (int)round_up((size_t)a.c.n_seqs * 4, 16);
     const int per_sm = (228 << 10) / (smem + 2304) < AttCfg<D, NB>::ctas ? (228 << 10) / (smem + 2304) : AttCfg<D, NB>::ctas;
     int64_t ctas = (int64_t)sms * per_sm;
-    if (ctas > most_ctas(D)) ctas = most_ctas(D);
+    if (ctas > kMaxSms * AttCfg<D, NB>::ctas) ctas = kMaxSms * AttCfg<D, NB>::ctas;
     if (ctas > most) ctas = most;
     static std::atomic<unsigned> ready;
     const auto kern = attend_kernel<T, D, NB>;
-    cudaError_t e = allow_smem((const void*)kern, ring + MOE_W4_MAX_SEQS * 4, ready, dev);
+    cudaError_t e = allow_smem((const void*)kern, ring + q_bytes(D, NB) + MOE_W4_MAX_SEQS * 4, ready, dev);
     if (e != cudaSuccess) return e;
     // Rows can be cut only where there are more tiles than rows; CTAs that share a
     // row wait for one another, so all must be resident.
@@ -889,9 +936,13 @@ static cudaError_t launch_attend(const AttendArgs& a, cudaStream_t st) {
 
 template <typename T>
 static cudaError_t launch_attend_dim(int dim, const AttendArgs& a, cudaStream_t st) {
-    if (a.group <= 8)
-        return dim == 64 ? launch_attend<T, 64, 1>(a, st) : dim == 128 ? launch_attend<T, 128, 1>(a, st) : launch_attend<T, 256, 1>(a, st);
-    return dim == 64 ? launch_attend<T, 64, 2>(a, st) : dim == 128 ? launch_attend<T, 128, 2>(a, st) : launch_attend<T, 256, 2>(a, st);
+    const int blocks = (a.block_heads + 7) / 8;
+    if (dim == 256) return blocks == 1 ? launch_attend<T, 256, 1>(a, st) : launch_attend<T, 256, 2>(a, st);
+    if (dim == 128)
+        return blocks == 1 ? launch_attend<T, 128, 1>(a, st)
+               : blocks == 2 ? launch_attend<T, 128, 2>(a, st) : launch_attend<T, 128, 3>(a, st);
+    return blocks == 1 ? launch_attend<T, 64, 1>(a, st)
+           : blocks == 2 ? launch_attend<T, 64, 2>(a, st) : launch_attend<T, 64, 3>(a, st);
 }
 
 static int check_heads(const moe_w4_kv_cache& c, int n_q_heads, int max_len) {
@@ -937,7 +988,8 @@ int moe_w4_attend_decode(const moe_w4_kv_cache* c, int n_q_heads, const void* q,
     a.out_stride = out_stride;
     a.n_q_heads = n_q_heads;
     a.group = n_q_heads / c->n_kv_heads;
-    a.head_blocks = (a.group + kHeads - 1) / kHeads;
+    a.head_blocks = (a.group + most_heads(c->head_dim) - 1) / most_heads(c->head_dim);
+    a.block_heads = (a.group + a.head_blocks - 1) / a.head_blocks;
     a.max_len = max_len;
     a.scale_log2 = scale * kLog2e;
     a.part_o = reinterpret_cast<float*>(ws + w.part_o);

@@ -111,7 +111,8 @@ int moe_w4_kv_append(const moe_w4_kv_cache* c, const moe_w4_kv_track* track, int
  * A sequence of length 0, or whose scores are all -inf, gives zeros and lse
  * -inf.  Cache slots past the length are not read as numbers: they may hold
  * anything, NaN included.  MOE_W4_ERR_UNSUPPORTED where n_seqs * n_kv_heads *
- * (tiles of 64 tokens up to max_len + 1) * (blocks of 16 query heads) passes 2^31. */
+ * (tiles of 64 tokens up to max_len + 1) * (blocks of 24 query heads of a kv
+ * head, 16 at head_dim 256) passes 2^31. */
 size_t moe_w4_attend_workspace_size(const moe_w4_kv_cache* c, int n_q_heads, int max_len, int with_track);
 int moe_w4_attend_decode(const moe_w4_kv_cache* c, int n_q_heads, const void* q, int64_t q_stride, float scale,
                          int max_len, void* out, int64_t out_stride, float* lse, const moe_w4_kv_track* track,

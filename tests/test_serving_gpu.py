@@ -131,6 +131,18 @@ def test_attention_one_sequence_split_over_the_gpu(torch, sv, n, dim, group):
     check_attention(s, q, out, lse, 0.11)
 
 
+@pytest.mark.parametrize("dim,group", [(64, 12), (64, 17), (64, 24), (64, 33), (128, 12), (128, 17), (128, 24), (128, 25),
+                                       (128, 128), (256, 16), (256, 17), (256, 24)])
+@pytest.mark.parametrize("kv_heads,page,layout", [(1, 16, "head"), (3, 7, "slot")])
+def test_attention_large_groups(torch, sv, dim, group, kv_heads, page, layout):
+    """Blocks of query heads of every size, rows that one CTA ends and rows that several share."""
+    lens = [5000, 1, 0, 64, 65, 700, 129]
+    s = Setup(torch, sv, lens, kv_heads, dim, page, layout, seed=24 + group)
+    q = s.randn(len(lens), kv_heads * group, dim).to(s.dt)
+    out, lse = sv.attend_decode(s.cache, q, return_lse=True)
+    check_attention(s, q, out, lse, dim ** -0.5)
+
+
 def test_attention_many_short_sequences(torch, sv):
     lens = [(i * 37) % 130 for i in range(700)]
     s = Setup(torch, sv, lens, 1, 64, 16, "head", seed=3)
