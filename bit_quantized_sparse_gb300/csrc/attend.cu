@@ -7,7 +7,7 @@
 // share them: 4 D bytes per token and kv head for 4 D group flops, so HBM
 // bounds it, and only the tensor pipe keeps the products out of the way (fp32
 // FMAs would already bound it at a group of 8).  mma.sync is enough here: a
-// tcgen05 tile of 128 rows would be nearly empty at 1 to 16 query heads.
+// tcgen05 tile of 128 rows would be nearly empty at 1 to 24 query heads.
 //
 // Work split.  A row is a (sequence, kv head, block of up to 24 query heads);
 // its tokens are cut into tiles of 64.  The tiles of all rows, in order, form
@@ -80,7 +80,7 @@ struct AttendArgs {
     const uint4* v;
     uint32_t page_pieces, head_pieces, slot_pieces;
     int n_q_heads, group, head_blocks, block_heads, max_len;   // a kv head's query heads in blocks
-    int runs;           // pages of a multiple of 16 slots: 16 tokens are one run in memory
+    int runs;           // 16 tokens are 1 or 2 runs in memory (pages of a multiple of 16 or 8 slots), or 0: any
     float scale_log2;   // scale * log2(e)
     float* part_o;      // [2 * CTAs][8 NB][D] unnormalised outputs
     float* part_ml;     // [2 * CTAs][8 NB][2] running maximum (log2) and sum
@@ -377,6 +377,7 @@ __global__ void __launch_bounds__(kAttThreads, AttCfg<D, NB>::ctas) attend_kerne
     constexpr int UNIT = unit_bytes(D);              // keys or values of 16 tokens
     constexpr int CH = D / 8;                        // 16-byte pieces of a row
     constexpr int PER = 32 / CH, STEPS = kSub / PER; // rows of a warp-wide copy
+    constexpr int HALF = STEPS / 2;                  // copies of 8 rows
     constexpr int TURN = 8 / PER;                    // copies until the swizzle repeats
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int g = lane >> 2, t4 = lane & 3;
@@ -421,7 +422,7 @@ __global__ void __launch_bounds__(kAttThreads, AttCfg<D, NB>::ctas) attend_kerne
     int token = at.tile * kTile + warp * kSub + (lane & 15);   // of ld's tile, this lane's to look up
     int page = -1;                 // of token
     uint64_t head_off = 0;         // of ld's row
-    uint64_t off = 0;              // of ld's tile: this lane's first piece of a run, or its token's row
+    uint64_t off = 0;              // of ld's tile: this lane's first piece of the run, its token's run, or its token's row
     bool run = false, any = false, there = false;
     auto read_page = [&](const Place& p, int t) {   // the page of token t of p's row
         int v = -1;
@@ -444,9 +445,9 @@ __global__ void __launch_bounds__(kAttThreads, AttCfg<D, NB>::ctas) attend_kerne
             if (bad) raise_status(&a.ctrl->status, MOE_W4_STATUS_BAD_INDEX);
             run = false;
         }
-        // of a run every lane's token is in one page; a lane starts at row row0 of it
-        const uint32_t r = run ? in - (lane & 15) + row0 : in;
-        off = head_off + (uint64_t)(uint32_t)page * a.page_pieces + (uint64_t)r * a.slot_pieces + (run ? piece : 0);
+        // of one run a lane starts row0 rows and a piece on; of two it knows its token's
+        const uint32_t r = run ? a.runs == 1 ? in - (lane & 15) + row0 : in - (lane & 7) : in;
+        off = head_off + (uint64_t)(uint32_t)page * a.page_pieces + (uint64_t)r * a.slot_pieces + (run && a.runs == 1 ? piece : 0);
     };
     uint32_t swizzle[TURN];        // of this lane's piece in the rows that it copies
 #pragma unroll
@@ -455,17 +456,25 @@ __global__ void __launch_bounds__(kAttThreads, AttCfg<D, NB>::ctas) attend_kerne
     const bool packed = a.slot_pieces == CH;   // a run's rows follow one another
     auto load = [&](uint32_t base, const uint4* pool) {
         if (run) {
-            const uint4* p = pool + off;
             uint32_t to[TURN];
 #pragma unroll
             for (int i = 0; i < TURN; ++i) to[i] = base + swizzle[i];
-            if (packed) {
+            const uint64_t step = (uint64_t)PER * a.slot_pieces;
+            if (a.runs == 2) {
+                const uint64_t other = __shfl_xor_sync(0xffffffffu, off, 8), more = (uint64_t)row0 * a.slot_pieces + piece;
+                const uint4* p = pool + (lane & 8 ? other : off) + more;
+                const uint4* p8 = pool + (lane & 8 ? off : other) + more;
+#pragma unroll
+                for (int i = 0; i < STEPS; ++i)
+                    cp_async_16_to(to[i % TURN] + i * PER * ROW, (i < HALF ? p : p8) + i % HALF * step, policy);
+            } else if (packed) {
+                const uint4* p = pool + off;
 #pragma unroll
                 for (int i = 0; i < STEPS; ++i) cp_async_16_to(to[i % TURN] + i * PER * ROW, p + i * PER * CH, policy);
             } else {
-                const uint32_t step = PER * a.slot_pieces;
+                const uint4* p = pool + off;
 #pragma unroll
-                for (int i = 0; i < STEPS; ++i) cp_async_16_to(to[i % TURN] + i * PER * ROW, p + (uint64_t)i * step, policy);
+                for (int i = 0; i < STEPS; ++i) cp_async_16_to(to[i % TURN] + i * PER * ROW, p + i * step, policy);
             }
         } else if (any) {
 #pragma unroll 1
@@ -1001,7 +1010,7 @@ int moe_w4_attend_decode(const moe_w4_kv_cache* c, int n_q_heads, const void* q,
     a.page_pieces = (uint32_t)(c->page_stride / 8);
     a.head_pieces = (uint32_t)(c->head_stride / 8);
     a.slot_pieces = (uint32_t)(c->slot_stride / 8);
-    a.runs = c->page_size % kSub == 0;
+    a.runs = c->page_size % 16 == 0 ? 1 : c->page_size % 8 == 0 ? 2 : 0;
     if (track) {
         a.lse2 = reinterpret_cast<float*>(ws + w.lse2);
         a.scores = reinterpret_cast<float*>(ws + w.scores);

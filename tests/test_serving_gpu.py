@@ -143,6 +143,19 @@ def test_attention_large_groups(torch, sv, dim, group, kv_heads, page, layout):
     check_attention(s, q, out, lse, dim ** -0.5)
 
 
+@pytest.mark.parametrize("dim,group", [(64, 4), (64, 24), (128, 6), (128, 16), (256, 8), (256, 12)])
+@pytest.mark.parametrize("page", [8, 24, 40])
+@pytest.mark.parametrize("layout", ["head", "slot"])
+def test_attention_pages_of_eights(torch, sv, dim, group, page, layout):
+    """Pages of a multiple of 8 slots but not of 16: two runs to 16 tokens, often on two pages."""
+    lens = [3000, 8, 9, 24, 511, 130]
+    s = Setup(torch, sv, lens, 2, dim, page, layout, seed=page)
+    q = s.randn(len(lens), 2 * group, dim).to(s.dt)
+    out, lse = sv.attend_decode(s.cache, q, return_lse=True)
+    assert s.cache.status() == 0
+    check_attention(s, q, out, lse, dim ** -0.5)
+
+
 def test_attention_many_short_sequences(torch, sv):
     lens = [(i * 37) % 130 for i in range(700)]
     s = Setup(torch, sv, lens, 1, 64, 16, "head", seed=3)
