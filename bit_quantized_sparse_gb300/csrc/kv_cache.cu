@@ -111,10 +111,11 @@ constexpr int kKeyRoom = 40 * 1024;              // keys that a CTA holds in sha
 // (4112 to 4096 tokens: 12.0 us with 4, 11.0 with 5, 11.3 with 8).
 constexpr int kKeyUnroll = 5;
 constexpr int kEvictUnroll = 4;                  // row pieces in flight of a thread
-// Bytes that the selecting CTAs move at most (as many as the lengths allow); more
-// go to a kernel on every SM.  16 x 4112 to 4096: 11.0 us inline, 12.0 with the
-// kernel; 4 x 32768 to 8192 (8 CTAs a row): 39.8 inline, 24.7 with it.
-constexpr int64_t kInlineMoveBytes = 4 << 20;
+// Tokens of a row that the selecting CTAs move at most (as many as the lengths
+// allow); more go to a kernel of their own on every SM.  2048 tokens kept of 16 x 8
+// rows of 128: 64 moved 10.0 us inline and 14.1 with the kernel, 128 moved 11.7 and
+// 14.6; of 2 rows of 256: 128 moved 12.6 and 12.0, 512 moved 22.0 and 12.4.
+constexpr int64_t kInlineMoves = 128;
 constexpr int kMovePairs = 64;                   // tokens moved at a time by a CTA
 
 struct alignas(16) EvictShared {
@@ -556,10 +557,8 @@ int moe_w4_kv_evict(const moe_w4_kv_cache* c, const moe_w4_kv_track* track, cons
     a.holes = reinterpret_cast<int32_t*>(ws + MOE_W4_CTRL_BYTES + kSyncBytes);
     a.movers = reinterpret_cast<int32_t*>(ws + MOE_W4_CTRL_BYTES + kSyncBytes + evict_list_bytes(*c, places));
     a.status = reinterpret_cast<unsigned int*>(ws);
-    // Many moves want every SM: a kernel of their own.  Few are done by the CTAs
-    // that selected them, which saves its start.
     const int64_t most = places < max_len - places ? places : max_len - places;
-    if (most * (int64_t)rows * c->head_dim * 8 > kInlineMoveBytes)
+    if (most > kInlineMoves)
         a.moved = reinterpret_cast<int32_t*>(ws + MOE_W4_CTRL_BYTES + kSyncBytes + 2 * evict_list_bytes(*c, places));
     const cudaError_t e = c->head_dim == 64 ? launch_evict<8>(a, (int)rows, stream)
                           : c->head_dim == 128 ? launch_evict<16>(a, (int)rows, stream) : launch_evict<32>(a, (int)rows, stream);
