@@ -95,7 +95,7 @@ struct EvictArgs {
     int budget, sink, recent, max_len, key_room;
     int32_t* holes;          // [row][budget]
     int32_t* movers;         // [row][budget]
-    int32_t* moved;          // [row] pairs in the lists, or NULL: the selecting CTAs move them too
+    int32_t* moved;          // [row] pairs in the lists, written for every row, or NULL: the selecting CTAs move them too
     unsigned int* heads_in;  // [n_seqs] heads that have read the length; zero between calls
     unsigned int* status;
 };
@@ -340,6 +340,9 @@ __global__ void __launch_bounds__(NT, 1024 / NT) kv_evict_kernel(const EvictArgs
         a.lens_out[b] = min(n, a.budget);
     }
     if (!cut) {
+        // Nothing moves.  The word has to say so: it holds what an earlier call, of any
+        // operator, left in the workspace.
+        if (a.moved && rank == 0 && tid == 0) a.moved[r] = 0;
         sync();   // CTA 0's memory stays until its length has been read
         return;
     }
