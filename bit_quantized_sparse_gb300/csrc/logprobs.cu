@@ -411,6 +411,9 @@ __global__ void __launch_bounds__(NT, kLpPerSm / NT) token_logprobs_kernel(const
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int rank = (int)cluster_rank(), ctas = (int)cluster_size();
     const int first = blockIdx.x / ctas, step = gridDim.x / ctas;
+    // CTA 0's shared memory may be written by the others once it runs: all say so
+    // here, and wait for it when they have their parts
+    if (NT == 256 && ctas > 1) cluster_arrive();
     griddep_wait();
 
     // the next vector of this thread to load, and how many of its row are left
@@ -523,6 +526,7 @@ __global__ void __launch_bounds__(NT, kLpPerSm / NT) token_logprobs_kernel(const
         const int kk = min(a.top, p.count);
         if (kk) word = part_top(p, most, scalar, kk, sh);
         else __syncthreads();
+        if (NT == 256 && ctas > 1 && r == first) cluster_wait();
         if (warp == 0) {
             s = warp_join(lane < (NT / 32) ? sh.sums[lane] : Sums{-INFINITY, 0.f, 0.f});
             if (NT == 256 && ctas > 1) {

@@ -63,6 +63,9 @@ MW4_DEV uint32_t cluster_size() {
 MW4_DEV void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
+// The same in two halves, for what needs no order of memory: that all CTAs run.
+MW4_DEV void cluster_arrive() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
+MW4_DEV void cluster_wait() { asm volatile("barrier.cluster.wait.aligned;" ::: "memory"); }
 // This place of shared memory in CTA `rank` of the cluster.
 MW4_DEV uint32_t at_rank(const void* p, int rank) {
     uint32_t a;

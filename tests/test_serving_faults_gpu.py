@@ -3,7 +3,7 @@ import numpy as np
 import pytest
 
 from oracle import serving_oracle as SO
-from tests.test_serving_gpu import Setup, check_evict, f64, sv, torch  # noqa: F401  (fixtures among them)
+from tests.test_serving_gpu import Setup, check_evict, check_logprobs, f64, sv, torch  # noqa: F401  (fixtures among them)
 
 pytestmark = pytest.mark.gpu
 
@@ -44,3 +44,20 @@ def test_evict_after_attention_in_the_same_workspace(torch, sv, track):
     assert len(s.cache._kept) == 1   # one workspace served both
     sv.attend_decode(s.cache, q, weight_out=torch.empty_like(s.weight) if track else None)
     check_evict(torch, sv, s, s.lens + 9, 301, 3, 20, True)
+
+
+# ---- log probabilities: clusters with the least to do before their parts meet ----
+@pytest.mark.parametrize("dtype,vector", [("float32", 4), ("bfloat16", 8), ("float16", 8)])
+@pytest.mark.parametrize("rows,ctas", [(1, 2), (1, 8), (7, 4), (57, 4), (57, 8), (114, 4), (228, 2)])
+@pytest.mark.parametrize("top", [0, 20])
+def test_logprobs_smallest_parts(torch, sv, dtype, vector, rows, ctas, top):
+    """A vector a thread: the CTAs of a row start and finish almost together.  The same bytes every time."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(rows + ctas)
+    x = (torch.randn(rows, 256 * ctas * vector, device="cuda", generator=g) * 3).to(getattr(torch, dtype))
+    t = torch.randint(0, x.shape[1], (rows,), device="cuda", generator=g).to(torch.int32)
+    check_logprobs(torch, sv, x, t, top)
+    first = sv.token_logprobs(x, t, top)
+    for _ in range(50):
+        for a, b in zip(first, sv.token_logprobs(x, t, top)):
+            assert a is b is None or torch.equal(a, b)
