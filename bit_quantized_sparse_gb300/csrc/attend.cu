@@ -46,7 +46,6 @@ constexpr int kSub = 16;                        // tokens of a warp's part of a 
 constexpr int kTile = kSub * kAttWarps;
 constexpr int most_heads(int dim) { return dim == 256 ? 16 : 24; }   // query heads of a row
 constexpr int kMaxSms = 160;                    // SMs that the workspace has room for
-constexpr float kLazyRescale = 8.f;             // log2 growth of the maximum before a rescale
 
 // Ring units per warp and CTAs per SM for a head size: 130 to 175 KB of every SM
 // hold units in flight.  One more unit makes the queue longer, not the copies
@@ -83,7 +82,7 @@ struct AttendArgs {
     int runs;           // 16 tokens are 1 or 2 runs in memory (pages of a multiple of 16 or 8 slots), or 0: any
     float scale_log2;   // scale * log2(e)
     float* part_o;      // [2 * CTAs][8 NB][D] unnormalised outputs
-    float* part_ml;     // [2 * CTAs][8 NB][2] running maximum (log2) and sum
+    float* part_ml;     // [2 * CTAs][8 NB][2] reference (log2) and sum of 2^(score - reference)
     RowSync* sync;      // [CTAs]
     float* scores;      // [n_seqs][n_q_heads][score_stride] log2 scores, or NULL
     float* lse2;        // [n_seqs][n_q_heads] log2 of the sums, with scores
@@ -94,8 +93,16 @@ struct AttendArgs {
     Ctrl* ctrl;
 };
 
+// Probabilities are taken against a reference that lies kBelow under the running
+// maximum (log2), so that the largest is 2^kBelow, and that follows it when it has
+// grown by more than kLazy.  bf16 has fp32's range.  fp16 ends at 2^16 and has no
+// step below 2^-24: with 13 + 2 the largest product term is 2^15 and the step
+// 2^-37 of a warp's largest probability.  (Against the maximum itself it was 2^-24:
+// where a first token without a value takes nearly all the weight and the output is
+// that of tokens 18 nats below it, it was off by up to 54%; now by its rounding.)
 template <typename T> struct Elem;
 template <> struct Elem<__nv_bfloat16> {
+    static constexpr float kBelow = 0.f, kLazy = 8.f;
     MW4_DEV static uint32_t pack(float a, float b) {
         __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
         return *reinterpret_cast<uint32_t*>(&v);
@@ -108,6 +115,7 @@ template <> struct Elem<__nv_bfloat16> {
     }
 };
 template <> struct Elem<__half> {
+    static constexpr float kBelow = 13.f, kLazy = 2.f;
     MW4_DEV static uint32_t pack(float a, float b) {
         __half2 v = __floats2half2_rn(a, b);
         return *reinterpret_cast<uint32_t*>(&v);
@@ -228,7 +236,7 @@ MW4_DEV void next_row(const int* lens, int n_seqs, int rows, Place& p) {
     p.tiles = tiles_of(p.len);
 }
 
-// lse from a head's maximum (log2) and sum; none: no token, or none with a score
+// lse from a head's reference (log2) and sum; none: no token, or none with a score
 // above -inf.
 MW4_DEV void write_lse(const AttendArgs& a, int b, int head, float M, float L, bool none) {
     const float lse2 = none ? -INFINITY : M + log2f(L);
@@ -750,19 +758,19 @@ __global__ void __launch_bounds__(kAttThreads, AttCfg<D, NB>::ctas) attend_kerne
                                 a.scores[((int64_t)at.b * a.n_q_heads + head0 + h) * a.score_stride + t] = s[n][0][e];
                         }
                 }
-                // The maximum that the exponents are taken against follows the true one
-                // only when it is exceeded by more than 2^8: fp32 sums hold the range, and
+                // The reference that the exponents are taken against follows the maximum
+                // only when that has grown by more than kLazy: fp32 sums hold the range, and
                 // the maximum is found and the output rescaled a few times a row.
 #pragma unroll
                 for (int n = 0; n < NB; ++n)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) grow |= s[n][0][e] > m[n][e & 1] + kLazyRescale;
+                    for (int e = 0; e < 4; ++e) grow |= s[n][0][e] > m[n][e & 1] + (Elem<T>::kBelow + Elem<T>::kLazy);
                 if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
                     for (int n = 0; n < NB; ++n)
 #pragma unroll
                         for (int c = 0; c < 2; ++c) {
-                            float to = fmaxf(m[n][c], fmaxf(s[n][0][c], s[n][0][c + 2]));
+                            float to = fmaxf(m[n][c], fmaxf(s[n][0][c], s[n][0][c + 2]) - Elem<T>::kBelow);
 #pragma unroll
                             for (int x = 4; x < 32; x <<= 1) to = fmaxf(to, __shfl_xor_sync(0xffffffffu, to, x));
                             const float f = m[n][c] == -INFINITY ? 0.f : ex2(m[n][c] - to);
@@ -776,7 +784,8 @@ __global__ void __launch_bounds__(kAttThreads, AttCfg<D, NB>::ctas) attend_kerne
                         }
                 }
                 // Probabilities enter the product as two 16-bit terms, about 16 (bf16) or 22
-                // (fp16) bits: one alone would cost as much accuracy as the output's rounding.
+                // (fp16, or down to its smallest step) bits: one alone would cost as much
+                // accuracy as the output's rounding.
 #pragma unroll
                 for (int n = 0; n < NB; ++n) {
                     const float r0 = m[n][0] == -INFINITY ? 0.f : m[n][0], r1 = m[n][1] == -INFINITY ? 0.f : m[n][1];

@@ -97,8 +97,10 @@ int moe_w4_kv_append(const moe_w4_kv_cache* c, const moe_w4_kv_track* track, int
  * CTAs that share a sequence wait for one another, with a limit, so the launch is
  * cooperative; moe_w4_test_skip_publish on its workspace makes those waits run out.
  * Query heads h * group .. h * group + group - 1 (group = n_q_heads /
- * n_kv_heads, at most 128) share kv head h.  Scores, softmax and sums are
- * fp32; out is rounded once.
+ * n_kv_heads, at most 128) share kv head h.  Scores, maxima and sums are fp32;
+ * probabilities are two 16-bit terms of the cache's type in the product with v:
+ * off by at most 2^-17 (bf16), or 2^-21 and 2^-38 of the row's largest (fp16);
+ * out is rounded once.
  *   q, out [n_seqs][n_q_heads][head_dim] of the cache's type, sequences
  *          q_stride (out_stride) elements apart, multiples of 8; 16-byte
  *          aligned
