@@ -432,6 +432,7 @@ __global__ void __launch_bounds__(kAttThreads, AttCfg<D, NB>::ctas) attend_kerne
     uint64_t head_off = 0;         // of ld's row
     uint64_t off = 0;              // of ld's tile: this lane's first piece of the run, its token's run, or its token's row
     bool run = false, any = false, there = false;
+    bool bad_pages = false;        // the warp has met a page outside the cache
     auto read_page = [&](const Place& p, int t) {   // the page of token t of p's row
         int v = -1;
         if (t < p.len) {
@@ -452,6 +453,7 @@ __global__ void __launch_bounds__(kAttThreads, AttCfg<D, NB>::ctas) attend_kerne
         if (__any_sync(0xffffffffu, bad)) {
             if (bad) raise_status(&a.ctrl->status, MOE_W4_STATUS_BAD_INDEX);
             run = false;
+            bad_pages = true;
         }
         // of one run a lane starts row0 rows and a piece on; of two it knows its token's
         const uint32_t r = run ? a.runs == 1 ? in - (lane & 15) + row0 : in - (lane & 7) : in;
@@ -741,12 +743,22 @@ __global__ void __launch_bounds__(kAttThreads, AttCfg<D, NB>::ctas) attend_kerne
                 for (int n = 0; n < NB; ++n)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) s[n][0][e] = (s[n][0][e] + s[n][1][e]) * a.scale_log2;
-                if (t0 + kSub > at.len) {
+                if (t0 + kSub > at.len || bad_pages) {   // tokens past the length or without a page (zeros here)
+                    bool none[2];
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) none[r] = t0 + g + 8 * r >= at.len;
+                    if (bad_pages)   // rare, so looked up again
+#pragma unroll 1
+                        for (int r = 0; r < 2; ++r) {
+                            const bool off_page = (unsigned)read_page(at, t0 + g + 8 * r) >= (unsigned)a.c.num_pages;
+                            none[0] |= r == 0 && off_page;
+                            none[1] |= r == 1 && off_page;
+                        }
 #pragma unroll
                     for (int n = 0; n < NB; ++n)
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
-                            if (t0 + g + 8 * (e >> 1) >= at.len) s[n][0][e] = -INFINITY;
+                            if (none[e >> 1]) s[n][0][e] = -INFINITY;
                 }
                 if (a.scores) {
 #pragma unroll

@@ -111,7 +111,8 @@ int moe_w4_kv_append(const moe_w4_kv_cache* c, const moe_w4_kv_track* track, int
  *          of p_t over the kv head's query heads, for t < seq_lens[b] (fp32, the
  *          strides of track; may be track->weight).  track->pos is not used.
  * A sequence of length 0, or whose scores are all -inf, gives zeros and lse
- * -inf.  Cache slots past the length are not read as numbers: they may hold
+ * -inf.  Tokens on pages outside the cache take no part, as if they scored -inf
+ * (and set MOE_W4_STATUS_BAD_INDEX).  Cache slots past the length are not read as numbers: they may hold
  * anything, NaN included.  MOE_W4_ERR_UNSUPPORTED where n_seqs * n_kv_heads *
  * (tiles of 64 tokens up to max_len + 1) * (blocks of 24 query heads of a kv
  * head, 16 at head_dim 256) passes 2^31. */

@@ -61,3 +61,50 @@ def test_logprobs_smallest_parts(torch, sv, dtype, vector, rows, ctas, top):
     for _ in range(50):
         for a, b in zip(first, sv.token_logprobs(x, t, top)):
             assert a is b is None or torch.equal(a, b)
+
+
+# ---- attention: tokens on pages outside the cache take no part ----
+@pytest.mark.parametrize("dtype", ["bfloat16", "float16"])
+@pytest.mark.parametrize("dim,kv_heads,group", [(64, 1, 4), (64, 2, 16), (64, 1, 24), (128, 2, 8), (128, 1, 12), (128, 1, 20),
+                                                (256, 2, 8), (256, 1, 16)])
+@pytest.mark.parametrize("page", [1, 7, 8, 16, 64])
+def test_attention_leaves_bad_pages_out(torch, sv, dtype, dim, kv_heads, group, page):
+    """Scores far below 0, where a token that scores 0 would take everything; a sequence without any page left."""
+    lens = [100, 60, 1500, 0, 90, 33]
+    s = Setup(torch, sv, lens, kv_heads, dim, page, "slot", dtype, seed=page, track=True)
+    s.k.abs_()
+    q = -s.randn(len(lens), kv_heads * group, dim).abs().to(s.dt)
+    there = [torch.ones(n, dtype=torch.bool) for n in lens]
+    for b, p, value in [(0, 1, s.k.shape[0]), (2, 0, -1), (2, 900 // page, 2 ** 31 - 1), (2, 901 // page, -2 ** 31),
+                        (4, 89 // page, -7)] + [(5, p, -1) for p in range(-(-33 // page))]:
+        s.table[b, p] = value
+        there[b][p * page:(p + 1) * page] = False
+    before = s.weight.clone()
+    drawn = torch.full_like(s.weight, float("nan"))
+    out, lse = sv.attend_decode(s.cache, q, scale=0.3, return_lse=True, max_len=1500, weight_out=drawn)
+    assert s.cache.status() == 2
+    u, bf = torch.finfo(s.dt).eps / 2, dtype == "bfloat16"
+    pool_k, pool_v, table = f64(s.k), f64(s.v), s.table.cpu().numpy()
+    for b, n in enumerate(lens):
+        left = np.nonzero(there[b].numpy())[0]
+        m = len(left)
+        # the tokens left, a page each
+        at = table[b, left // page], slice(None), left % page
+        one = [x[at][:, :, None, :] if m else np.zeros((1, kv_heads, 1, dim)) for x in (pool_k, pool_v)]
+        want = SO.attend(f64(q[b:b + 1]), *one, np.arange(max(m, 1))[None], [m], 0.3)
+        for h, w in enumerate(want):
+            mine = slice(h * group, (h + 1) * group)
+            delta = (dim / 16 + 16 + 4) * 2.0 ** -24 * w["absqk"]
+            rel = 2 * delta + 2.0 ** -20 + (2.0 ** -17 if bf else 2.0 ** -21) + (n / 64 + 64) * 2.0 ** -24
+            tol = rel * w["absv"] + u * np.abs(w["out"]) + (0 if bf else 2.0 ** -38 * w["vsum"] / w["floor"]) + 2.0 ** -25
+            assert np.all(np.abs(f64(out[b, mine]) - w["out"]) <= tol), (b, h)
+            if m == 0:
+                assert np.all(np.isneginf(f64(lse[b, mine])))
+            else:
+                assert np.all(np.abs(f64(lse[b, mine]) - w["lse"]) <= delta + 2.0 ** -20 + (n / 64 + 64) * 2.0 ** -24
+                              + 8 * 2.0 ** -24 * (np.abs(w["lse"]) + w["absqk"]))
+            more = f64(drawn[b, h, :n]) - f64(before[b, h, :n])
+            assert np.all(more[~there[b].numpy()] == 0)
+            assert np.all(np.abs(more[left] - w["drawn"]) <= (2 * delta + 2.0 ** -19 + 8 * 2.0 ** -24 * (w["absqk"] + np.abs(w["lse"]).max(initial=0, where=np.isfinite(w["lse"])))
+                          + (n / 64 + 64) * 2.0 ** -24) * w["drawn"]
+                          + (group + 4) * 2.0 ** -24 * (f64(before[b, h, left]) + w["drawn"]))
