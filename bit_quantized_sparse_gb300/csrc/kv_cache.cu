@@ -160,12 +160,13 @@ MW4_DEV void move_pairs(const EvictArgs& a, int b, int h, int64_t row, const int
         const int64_t to = kv_offset(a.c, b, dst);
         if (from < 0 || to < 0) {
             raise_status(a.status, MOE_W4_STATUS_BAD_INDEX);
-            from = -1;
+            from = -1;   // the whole move is left out: the place keeps its own token's weight and position too
+        } else {
+            a.weight_out[row + dst] = w;
+            a.pos_out[row + dst] = p;
         }
         sh_from[tid] = from;
         sh_to[tid] = to;
-        a.weight_out[row + dst] = w;
-        a.pos_out[row + dst] = p;
     }
     __syncthreads();
     // keys of pair i are copy 2 i, its values copy 2 i + 1

@@ -126,8 +126,9 @@ int moe_w4_attend_decode(const moe_w4_kv_cache* c, int n_q_heads, const void* q,
  * seen[b] - recent; then the larger weight (NaN below every number, -0 equal
  * to 0); of equals the lower token index.  Tokens kept in place stay there;
  * the kept tokens at indexes >= budget move, in ascending order, into the
- * places below budget that were dropped, in ascending order: keys and values
- * inside the cache, and
+ * places below budget that were dropped, in ascending order (a move from or to a
+ * page outside the cache is left out: the place keeps its token, and
+ * MOE_W4_STATUS_BAD_INDEX is set): keys and values inside the cache, and
  *   lens_out[b]       = min(seq_lens[b], budget)
  *   weight_out, pos_out (strides of track) the weights and positions of the
  *                     tokens now at 0 .. lens_out[b] - 1

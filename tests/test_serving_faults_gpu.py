@@ -108,3 +108,38 @@ def test_attention_leaves_bad_pages_out(torch, sv, dtype, dim, kv_heads, group, 
             assert np.all(np.abs(more[left] - w["drawn"]) <= (2 * delta + 2.0 ** -19 + 8 * 2.0 ** -24 * (w["absqk"] + np.abs(w["lse"]).max(initial=0, where=np.isfinite(w["lse"])))
                           + (n / 64 + 64) * 2.0 ** -24) * w["drawn"]
                           + (group + 4) * 2.0 ** -24 * (f64(before[b, h, left]) + w["drawn"]))
+
+
+# ---- eviction: a move from or to a page outside the cache is left out as a whole ----
+@pytest.mark.parametrize("lens,budget", [([400, 300, 90], 280), ([2000, 900, 90], 300)])   # moves by the selecting CTAs, and by a kernel
+@pytest.mark.parametrize("in_place", [False, True])
+def test_evict_leaves_bad_pages_out(torch, sv, lens, budget, in_place):
+    s = Setup(torch, sv, lens, 2, 64, 16, seed=41, track=True)
+    for b, page, value in ((0, 0, -1), (0, 5, s.k.shape[0]), (0, budget // 16 + 2, 2 ** 31 - 1), (1, 3, -2 ** 31)):
+        s.table[b, page] = value
+    seen = s.lens + 5
+    k, v, w, p = f64(s.k), f64(s.v), f64(s.weight), s.pos.cpu().numpy().copy()
+    table, pages = s.table.cpu().numpy(), s.k.shape[0]
+    left_out = 0
+    for b, n in enumerate(lens):
+        for h in range(2) if n > budget else ():
+            kept = SO.kept_tokens(w[b, h, :n], p[b, h, :n], int(seen[b]), budget, 1, 9)
+            holes = sorted(set(range(budget)) - set(kept))
+            for to, frm in zip(holes, [j for j in kept if j >= budget]):
+                if not all(0 <= table[b, j // 16] < pages for j in (to, frm)):
+                    left_out += 1
+                    continue
+                for pool in (k, v):
+                    pool[table[b, to // 16], h, to % 16] = pool[table[b, frm // 16], h, frm % 16]
+                w[b, h, to], p[b, h, to] = w[b, h, frm], p[b, h, frm]
+    assert left_out
+    outs = {} if in_place else dict(lens_out=torch.zeros_like(s.lens), weight_out=torch.zeros_like(s.weight),
+                                    pos_out=torch.zeros_like(s.pos))
+    sv.kv_evict(s.cache, seen, budget, 1, 9, **outs)
+    assert s.cache.status() == 2
+    assert np.array_equal(f64(s.k), k, equal_nan=True) and np.array_equal(f64(s.v), v, equal_nan=True)
+    got_w, got_p = f64(outs.get("weight_out", s.weight)), outs.get("pos_out", s.pos).cpu().numpy()
+    for b, n in enumerate(lens):
+        m = min(n, budget)
+        assert np.array_equal(got_w[b, :, :m], w[b, :, :m]) and np.array_equal(got_p[b, :, :m], p[b, :, :m])
+    assert outs.get("lens_out", s.lens).tolist() == [min(n, budget) for n in lens]
