@@ -8,7 +8,7 @@ it (`attend_decode`), cutting it to a budget by accumulated attention weight
 
 Every call is enqueued on `stream` (default: the current stream) and returns at
 once; what it allocates belongs to that stream, tensors given to it must be
-ready there.  Arguments are checked here (ValueError) and in the library
+ready there, and they and the stream belong to the current GPU.  Arguments are checked here (ValueError) and in the library
 (moe_w4.MoeW4Error); indexes in device memory are checked by the kernels, which
 leave out what is out of range and set the sticky status word
 (`PagedKVCache.status`, `logprobs_status`).  For use in a CUDA graph make one
@@ -38,8 +38,18 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
 def _handle(stream, device):
-    return _raw_stream(device.index) if stream is None else stream.cuda_stream
+    """The handle to launch on.  The library takes the current GPU, so tensors and stream have to be its own."""
+    if device.index != _current_device():
+        raise ValueError("tensors on %s, which is not the current GPU" % device)
+    if stream is None:
+        return _raw_stream(device.index)
+    if stream.device != device:
+        raise ValueError("a stream of the tensors' GPU")
+    return stream.cuda_stream
 
 
 def _empty(stream, shape, dtype, device):

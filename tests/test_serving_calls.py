@@ -1,0 +1,88 @@
+"""The calls of serving.py around the library, without a GPU: tensors are stand-ins that say they lie on one, and the
+library's entry points are replaced, so that nothing is launched."""
+import os
+from types import SimpleNamespace
+
+import pytest
+
+torch = pytest.importorskip("torch")
+
+
+class Fake:
+    """What serving.py asks of a CUDA tensor."""
+    is_cuda = True
+
+    def __init__(self, shape, dtype, device):
+        self.shape, self.dtype, self.device = torch.Size(shape), dtype, torch.device(device)
+        self._stride = torch.empty(self.shape, device="meta").stride()
+
+    def dim(self):
+        return len(self.shape)
+
+    def stride(self, d=None):
+        return self._stride if d is None else self._stride[d]
+
+    def data_ptr(self):
+        return 4096
+
+
+@pytest.fixture
+def sv():
+    from bit_quantized_sparse_gb300 import _build
+    if not os.path.exists(_build.LIB):
+        _build.build()
+    from bit_quantized_sparse_gb300 import serving
+    return serving
+
+
+@pytest.fixture
+def calls(sv, monkeypatch):
+    """The library's calls by name, with their arguments; every one succeeds.  GPU 0 is current."""
+    made = []
+    for name in ("moe_w4_kv_append", "moe_w4_attend_decode", "moe_w4_kv_evict", "moe_w4_token_logprobs",
+                 "moe_w4_workspace_init"):
+        monkeypatch.setattr(sv.mw, name, lambda *a, name=name: made.append((name, a)) or 0)
+    monkeypatch.setattr(sv, "_raw_stream", lambda index: 0)
+    monkeypatch.setattr(sv, "_current_device", lambda: 0, raising=False)
+    monkeypatch.setattr(sv, "_empty", lambda stream, shape, dtype, device: Fake(shape, dtype, device))
+    monkeypatch.setattr(sv, "_ctrl", {})
+    monkeypatch.setattr(sv, "_capturing", lambda stream: False, raising=False)
+    return made
+
+
+def cache(sv, device="cuda:0", seqs=2, pages=4, page=16, heads=2, dim=64, slots=None):
+    kv = [Fake((8, heads, page, dim), torch.bfloat16, device) for _ in range(2)]
+    shape = (seqs, heads, slots or pages * page)
+    return sv.PagedKVCache(*kv, Fake((seqs, pages), torch.int32, device), Fake((seqs,), torch.int32, device),
+                           Fake(shape, torch.float32, device), Fake(shape, torch.int32, device))
+
+
+def every_call(sv, device="cuda:0", stream=None):
+    """One call of each operator, as functions."""
+    c = cache(sv, device)
+    q = Fake((2, 4, 64), torch.bfloat16, device)
+    new = Fake((2, 2, 64), torch.bfloat16, device)
+    seen = Fake((2,), torch.int32, device)
+    x = Fake((3, 100), torch.float32, device)
+    return c, [lambda: sv.kv_append(c, new, new, stream=stream), lambda: sv.attend_decode(c, q, stream=stream),
+               lambda: sv.kv_evict(c, seen, 32, stream=stream), lambda: sv.token_logprobs(x, top=3, stream=stream)]
+
+
+def test_calls_reach_the_library(sv, calls):
+    for call in every_call(sv)[1]:
+        call()
+    assert [name for name, _ in calls if name != "moe_w4_workspace_init"] == [
+        "moe_w4_kv_append", "moe_w4_attend_decode", "moe_w4_kv_evict", "moe_w4_token_logprobs"]
+
+
+@pytest.mark.parametrize("device,stream", [
+    ("cuda:1", None),                                                                     # tensors of a GPU that is not current
+    ("cuda:1", SimpleNamespace(cuda_stream=7, device=torch.device("cuda:1"))),
+    ("cuda:0", SimpleNamespace(cuda_stream=7, device=torch.device("cuda:1")))])           # a stream of another GPU
+def test_other_gpus_are_refused(sv, calls, device, stream):
+    """The library launches on the current GPU: tensors and streams of another one are refused, with nothing enqueued."""
+    c, every = every_call(sv, device, stream)
+    for call in every:
+        with pytest.raises(ValueError, match="GPU"):
+            call()
+    assert not calls and not c._ws and not c._kept and not sv._ctrl
