@@ -8,12 +8,13 @@ it (`attend_decode`), cutting it to a budget by accumulated attention weight
 
 Every call is enqueued on `stream` (default: the current stream) and returns at
 once; what it allocates belongs to that stream, tensors given to it must be
-ready there, and they and the stream belong to the current GPU.  Arguments are checked here (ValueError) and in the library
-(moe_w4.MoeW4Error); indexes in device memory are checked by the kernels, which
-leave out what is out of range and set the sticky status word
-(`PagedKVCache.status`, `logprobs_status`).  For use in a CUDA graph make one
-call of the same sizes on the capturing stream first, so that its workspace
-exists; the cache keeps every workspace that a graph may hold.
+ready there, and they and the stream belong to the current GPU.  Arguments are
+checked here (ValueError) and in the library (moe_w4.MoeW4Error); indexes in
+device memory are checked by the kernels, which leave out what is out of range
+and set the sticky status word (`PagedKVCache.status`, `logprobs_status`).  For
+use in a CUDA graph make one call of the same sizes on the capturing stream
+first, so that its workspace exists (RuntimeError otherwise); the cache keeps
+every workspace that a graph may hold.
 """
 from __future__ import annotations
 
@@ -59,8 +60,18 @@ def _empty(stream, shape, dtype, device):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
+def _capturing(stream):
+    if stream is None:
+        return torch.cuda.is_current_stream_capturing()
+    with torch.cuda.stream(stream):
+        return torch.cuda.is_current_stream_capturing()
+
+
 def _new_workspace(nbytes, device, stream):
-    """`nbytes` of device memory of the call's stream, cleared there."""
+    """`nbytes` of device memory of the call's stream, cleared there: now, not whenever a graph runs."""
+    if _capturing(stream):
+        raise RuntimeError("the stream is being captured and has no workspace for this call: make one call of the same "
+                           "sizes on it before the capture")
     ws = _empty(stream, (nbytes,), torch.uint8, device)
     mw._check(mw.moe_w4_workspace_init(ws.data_ptr(), nbytes, _handle(stream, device)), "workspace_init")
     return ws

@@ -86,3 +86,31 @@ def test_other_gpus_are_refused(sv, calls, device, stream):
         with pytest.raises(ValueError, match="GPU"):
             call()
     assert not calls and not c._ws and not c._kept and not sv._ctrl
+
+
+@pytest.mark.parametrize("which", range(4))
+def test_first_call_in_a_capture_is_refused(sv, calls, monkeypatch, which):
+    """A workspace made while its stream is captured would be cleared by the graph only, and taken for clear before."""
+    stream = SimpleNamespace(cuda_stream=9, device=torch.device("cuda:0"))
+    c, every = every_call(sv, stream=stream)
+    monkeypatch.setattr(sv, "_capturing", lambda s: s is stream)
+    with pytest.raises(RuntimeError, match="captur"):
+        every[which]()
+    assert not calls and not c._ws and not c._kept and not sv._ctrl
+    monkeypatch.setattr(sv, "_capturing", lambda s: False)
+    every[which]()                                             # the call outside
+    made = len(calls)
+    monkeypatch.setattr(sv, "_capturing", lambda s: True)
+    every[which]()                                             # may be captured then
+    assert len(calls) == made + 1 and calls[-1][0] != "moe_w4_workspace_init"
+
+
+def test_larger_workspace_in_a_capture_is_refused(sv, calls, monkeypatch):
+    c, (append, attend, _, _) = every_call(sv)
+    append()
+    monkeypatch.setattr(sv, "_capturing", lambda s: True)
+    append()
+    ws = dict(c._ws)
+    with pytest.raises(RuntimeError, match="captur"):
+        attend()                                               # needs a larger one than the append made
+    assert c._ws == ws and len(c._kept) == 1

@@ -143,3 +143,40 @@ def test_evict_leaves_bad_pages_out(torch, sv, lens, budget, in_place):
         m = min(n, budget)
         assert np.array_equal(got_w[b, :, :m], w[b, :, :m]) and np.array_equal(got_p[b, :, :m], p[b, :, :m])
     assert outs.get("lens_out", s.lens).tolist() == [min(n, budget) for n in lens]
+
+
+# ---- graphs: a stream's first call cannot be a captured one ----
+def test_first_call_in_a_capture_is_refused(torch, sv):
+    s = Setup(torch, sv, [100, 60], 2, 64, 16, seed=42, track=True)
+    q = s.randn(2, 8, 64).to(s.dt)
+    good = sv.attend_decode(s.cache, q)
+    x = torch.randn(3, 1000, device="cuda")
+    rows = sv.token_logprobs(x, top=4)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    known = len(sv._ctrl)
+    new, seen = s.randn(2, 2, 64).to(s.dt), s.lens.clone()
+    with torch.cuda.graph(torch.cuda.CUDAGraph(), stream=side):
+        first = torch.zeros(1, device="cuda")   # something to capture
+        for call in (lambda: sv.attend_decode(s.cache, q), lambda: sv.kv_append(s.cache, new, new),
+                     lambda: sv.kv_evict(s.cache, seen, 50), lambda: sv.token_logprobs(x, top=4)):
+            with pytest.raises(RuntimeError, match="captur"):
+                call()
+    del first
+    assert len(s.cache._ws) == 1 and len(sv._ctrl) == known
+    graphs = [torch.cuda.CUDAGraph() for _ in range(2)]
+    out = torch.empty_like(q)
+    with torch.cuda.stream(side):
+        sv.attend_decode(s.cache, q)
+        sv.token_logprobs(x, top=4)
+        side.synchronize()
+        for graph in graphs:                     # the second before the first has run
+            with torch.cuda.graph(graph, stream=side):
+                sv.attend_decode(s.cache, q, out=out)
+                got = sv.token_logprobs(x, top=4)
+    for graph in graphs[::-1]:
+        out.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, good)
+    assert torch.equal(got.top_index, rows.top_index) and s.cache.status() == 0
