@@ -11,10 +11,10 @@ once; what it allocates belongs to that stream, tensors given to it must be
 ready there, and they and the stream belong to the current GPU.  Arguments are
 checked here (ValueError) and in the library (moe_w4.MoeW4Error); indexes in
 device memory are checked by the kernels, which leave out what is out of range
-and set the sticky status word (`PagedKVCache.status`, `logprobs_status`).  For
-use in a CUDA graph make one call of the same sizes on the capturing stream
-first, so that its workspace exists (RuntimeError otherwise); the cache keeps
-every workspace that a graph may hold.
+and set the sticky status word (`PagedKVCache.status` and `reset`,
+`logprobs_status` and `logprobs_reset`).  For use in a CUDA graph make one call
+of the same sizes on the capturing stream first, so that its workspace exists
+(RuntimeError otherwise); the cache keeps every workspace that a graph may hold.
 """
 from __future__ import annotations
 
@@ -75,6 +75,14 @@ def _new_workspace(nbytes, device, stream):
     ws = _empty(stream, (nbytes,), torch.uint8, device)
     mw._check(mw.moe_w4_workspace_init(ws.data_ptr(), nbytes, _handle(stream, device)), "workspace_init")
     return ws
+
+
+def _clear(workspaces, device):
+    """Clears workspaces in place (graphs may hold their addresses), with the GPU idle before and after."""
+    torch.cuda.synchronize(device)
+    for ws in workspaces:
+        mw._check(mw.moe_w4_workspace_init(ws.data_ptr(), ws.numel(), _handle(None, device)), "workspace_init")
+    torch.cuda.synchronize(device)
 
 
 def _word(ws):
@@ -185,6 +193,11 @@ class PagedKVCache:
         for ws in self._kept:
             got |= _word(ws)
         return got
+
+    def reset(self) -> None:
+        """Clears the device status and the workspaces of this cache, all streams together, as has to be done after a
+        wait that ran out (synchronises).  Keys, values, lengths, weights and positions stay."""
+        _clear(self._kept, self.device)
 
 
 def _like(t, dtype, shape, device):
@@ -368,3 +381,9 @@ def logprobs_status() -> int:
     for ws in _ctrl.values():
         got |= _word(ws[1])
     return got
+
+
+def logprobs_reset() -> None:
+    """Clears the device status of token_logprobs calls on the current GPU, all streams together (synchronises)."""
+    device = torch.device("cuda", _current_device())
+    _clear([t for (index, _), (_, t) in _ctrl.items() if index == device.index], device)

@@ -114,3 +114,21 @@ def test_larger_workspace_in_a_capture_is_refused(sv, calls, monkeypatch):
     with pytest.raises(RuntimeError, match="captur"):
         attend()                                               # needs a larger one than the append made
     assert c._ws == ws and len(c._kept) == 1
+
+
+def test_reset_clears_every_workspace(sv, calls, monkeypatch):
+    """All that graphs may hold, in place, with the GPU idle before and after."""
+    monkeypatch.setattr(torch.cuda, "synchronize", lambda device=None: calls.append(("synchronize", ())))
+    monkeypatch.setattr(Fake, "numel", lambda self: self.shape.numel(), raising=False)
+    c, every = every_call(sv)
+    for call in every:
+        call()
+    sizes = [t.numel() for t in c._kept]
+    assert len(sizes) == 2                                     # the append's, and a larger one
+    kept, ctrl = list(c._kept), dict(sv._ctrl)
+    for reset, want in ((c.reset, sizes), (sv.logprobs_reset, [256])):
+        del calls[:]
+        reset()
+        assert [a[1] for name, a in calls if name == "moe_w4_workspace_init"] == want
+        assert calls[0][0] == calls[-1][0] == "synchronize"
+    assert c._kept == kept and sv._ctrl == ctrl

@@ -180,3 +180,43 @@ def test_first_call_in_a_capture_is_refused(torch, sv):
         torch.cuda.synchronize()
         assert torch.equal(out, good)
     assert torch.equal(got.top_index, rows.top_index) and s.cache.status() == 0
+
+
+# ---- status: cleared from Python ----
+def test_cache_reset_clears_the_status(torch, sv):
+    """After bad indexes, and after a wait that ran out (2 s), the cache is as new; its workspaces stay for graphs."""
+    from bit_quantized_sparse_gb300 import moe_w4 as mw
+    s = Setup(torch, sv, [4000, 70], 1, 64, 16, seed=43, track=True)
+    q = s.randn(2, 4, 64).to(s.dt)
+    good = sv.attend_decode(s.cache, q)
+    page = int(s.table[1, 0])
+    s.table[1, 0] = -1
+    sv.attend_decode(s.cache, q)
+    assert s.cache.status() == 2
+    s.cache.reset()
+    s.table[1, 0] = page
+    assert s.cache.status() == 0 and torch.equal(sv.attend_decode(s.cache, q), good) and s.cache.status() == 0
+    (ptr, size, _), = s.cache._ws.values()
+    assert mw.moe_w4_test_skip_publish(ptr, size, 1, torch.cuda.current_stream().cuda_stream) == 0
+    sv.attend_decode(s.cache, q)
+    assert s.cache.status() == 1
+    s.cache.reset()
+    for _ in range(3):
+        assert torch.equal(sv.attend_decode(s.cache, q), good) and s.cache.status() == 0
+    assert [w[0] for w in s.cache._ws.values()] == [ptr]
+
+
+def test_logprobs_reset_clears_the_status(torch, sv):
+    sv.logprobs_reset()
+    x = torch.randn(2, 500, device="cuda")
+    side = torch.cuda.Stream()
+    bad = torch.tensor([3, 500], dtype=torch.int32, device="cuda")
+    side.wait_stream(torch.cuda.current_stream())
+    sv.token_logprobs(x, bad, stream=side)
+    assert sv.logprobs_status() == 2
+    sv.logprobs_reset()
+    assert sv.logprobs_status() == 0
+    again = sv.token_logprobs(x, bad, stream=side)
+    assert sv.logprobs_status() == 2 and torch.isnan(again.logprob[1])
+    sv.logprobs_reset()
+    assert sv.logprobs_status() == 0
