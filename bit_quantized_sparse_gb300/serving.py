@@ -251,7 +251,8 @@ def attend_decode(cache: PagedKVCache, q, scale: Optional[float] = None, max_len
     """Attention of one new token per sequence, q [sequences][query heads][head dim], over its cached tokens.
 
     scale       of the scores (default 1/sqrt(head dim))
-    max_len     upper bound of seq_lens (default: what the block table can hold); a small one saves work
+    max_len     upper bound of seq_lens (default: what the block table, and the weights if they are added up, can
+                hold); a small one saves work
     return_lse  also return the log sum of the exponentials, fp32 [sequences][query heads]
     weight_out  fp32 tensor like cache.weight (it may be cache.weight itself): gets cache.weight plus the
                 probability that each token drew, summed over the kv head's query heads
@@ -273,12 +274,15 @@ def attend_decode(cache: PagedKVCache, q, scale: Optional[float] = None, max_len
     if q_stride < 0 or out_stride < 0:
         raise ValueError("q and out: contiguous heads")
     lse = _empty(stream, (shape[0], heads), torch.float32, device) if return_lse else None
-    max_len = cache.capacity if max_len is None else int(max_len)
     track = None
     if weight_out is not None:
         _need(cache.weight is not None, "weight_out needs a cache with weights")
         cache._check_like_weight(weight_out, torch.float32)
         track = cache._t
+    if max_len is None:
+        max_len = cache.capacity if track is None else min(cache.capacity, cache.weight.shape[2])
+    else:
+        max_len = int(max_len)
     handle = _handle(stream, device)
     key = (heads, max_len, weight_out is not None)
     size = cache._sizes.get(key)

@@ -132,3 +132,13 @@ def test_reset_clears_every_workspace(sv, calls, monkeypatch):
         assert [a[1] for name, a in calls if name == "moe_w4_workspace_init"] == want
         assert calls[0][0] == calls[-1][0] == "synchronize"
     assert c._kept == kept and sv._ctrl == ctrl
+
+
+def test_attention_of_a_cache_with_fewer_weights_than_places(sv, calls):
+    """With weights the default bound is what they have room for: the library refuses a larger one."""
+    c = cache(sv, slots=40)
+    q = Fake((2, 4, 64), torch.bfloat16, "cuda:0")
+    sv.attend_decode(c, q, weight_out=c.weight)
+    sv.attend_decode(c, q)
+    sv.attend_decode(c, q, max_len=7, weight_out=c.weight)
+    assert [a[5] for name, a in calls if name == "moe_w4_attend_decode"] == [40, 64, 7]
