@@ -34,6 +34,13 @@ def _need(ok, what):
         raise ValueError(what)
 
 
+def _int(n, what):
+    """A C int: ctypes would cut a larger number to 32 bits."""
+    if not -2 ** 31 <= n < 2 ** 31:
+        raise ValueError(what + ": a 32-bit integer")
+    return n
+
+
 # The current stream's handle without the Stream object around it, where torch offers that (a call saves 3 us).
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
@@ -282,7 +289,7 @@ def attend_decode(cache: PagedKVCache, q, scale: Optional[float] = None, max_len
     if max_len is None:
         max_len = cache.capacity if track is None else min(cache.capacity, cache.weight.shape[2])
     else:
-        max_len = int(max_len)
+        max_len = _int(int(max_len), "max_len")
     handle = _handle(stream, device)
     key = (heads, max_len, weight_out is not None)
     size = cache._sizes.get(key)
@@ -319,14 +326,15 @@ def kv_evict(cache: PagedKVCache, seen, budget: int, sink: int = 0, recent: int 
         pos_out = cache.pos
     else:
         cache._check_like_weight(pos_out, torch.int32)
-    max_len = min(cache.capacity, cache.weight.shape[2]) if max_len is None else int(max_len)
+    max_len = min(cache.capacity, cache.weight.shape[2]) if max_len is None else _int(int(max_len), "max_len")
+    budget, sink, recent = _int(int(budget), "budget"), _int(sink, "sink"), _int(recent, "recent")
     handle = _handle(stream, device)
-    key = (int(budget), max_len)
+    key = (budget, max_len)
     size = cache._sizes.get(key)
     if size is None:
         size = cache._sizes[key] = max(mw.moe_w4_evict_workspace_size(cache._c, *key), mw.CTRL_BYTES)
     ws = cache._workspace(size, stream, handle)
-    status = mw.moe_w4_kv_evict(cache._c, cache._t, seen.data_ptr(), key[0], sink, recent, max_len, lens_out.data_ptr(),
+    status = mw.moe_w4_kv_evict(cache._c, cache._t, seen.data_ptr(), budget, sink, recent, max_len, lens_out.data_ptr(),
                                 weight_out.data_ptr(), pos_out.data_ptr(), ws[0], ws[1], handle)
     if status:
         mw._check(status, "moe_w4_kv_evict")
@@ -357,6 +365,7 @@ def token_logprobs(logits, targets=None, top: int = 0, stream=None) -> TokenLogp
     device = logits.device
     if targets is not None:
         _check_index(targets, n, device, "targets")
+    top = _int(top, "top")
     handle = _handle(stream, device)
     key = (device.index, handle)
     ws = _ctrl.get(key)

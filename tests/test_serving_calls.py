@@ -142,3 +142,21 @@ def test_attention_of_a_cache_with_fewer_weights_than_places(sv, calls):
     sv.attend_decode(c, q)
     sv.attend_decode(c, q, max_len=7, weight_out=c.weight)
     assert [a[5] for name, a in calls if name == "moe_w4_attend_decode"] == [40, 64, 7]
+
+
+@pytest.mark.parametrize("kw", [dict(budget=2 ** 32 + 8), dict(sink=2 ** 32), dict(recent=2 ** 32 + 1), dict(max_len=2 ** 32 + 40),
+                                dict(budget=2 ** 31), dict(recent=-2 ** 32)])
+def test_eviction_refuses_numbers_past_32_bits(sv, calls, kw):
+    """The C ABI takes ints: cut to 32 bits, a budget of 2^32 + 8 would keep 8 tokens."""
+    with pytest.raises(ValueError, match=next(iter(kw))):
+        sv.kv_evict(cache(sv), Fake((2,), torch.int32, "cuda:0"), **{**dict(budget=32), **kw})
+    assert not calls
+
+
+def test_other_calls_refuse_numbers_past_32_bits(sv, calls):
+    q = Fake((2, 4, 64), torch.bfloat16, "cuda:0")
+    with pytest.raises(ValueError, match="max_len"):
+        sv.attend_decode(cache(sv), q, max_len=2 ** 32 + 5)
+    with pytest.raises(ValueError, match="top"):
+        sv.token_logprobs(Fake((2, 100), torch.float32, "cuda:0"), top=2 ** 32 + 3)
+    assert not calls
