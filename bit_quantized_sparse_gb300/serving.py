@@ -193,6 +193,13 @@ class PagedKVCache:
             ws = self._ws[handle] = (t.data_ptr(), nbytes, t)
         return ws
 
+    def _remember(self, key, size):
+        """Keeps a call's workspace size; a loop whose bound grows step by step asks for ever new ones."""
+        if len(self._sizes) >= 256:
+            self._sizes.clear()
+        size = self._sizes[key] = max(size, mw.CTRL_BYTES)
+        return size
+
     def status(self) -> int:
         """The device status of the calls on this cache, all streams together (synchronises)."""
         torch.cuda.synchronize(self.device)
@@ -294,8 +301,7 @@ def attend_decode(cache: PagedKVCache, q, scale: Optional[float] = None, max_len
     key = (heads, max_len, weight_out is not None)
     size = cache._sizes.get(key)
     if size is None:
-        size = max(mw.moe_w4_attend_workspace_size(cache._c, heads, max_len, key[2]), mw.CTRL_BYTES)
-        cache._sizes[key] = size
+        size = cache._remember(key, mw.moe_w4_attend_workspace_size(cache._c, heads, max_len, key[2]))
     ws = cache._workspace(size, stream, handle)
     status = mw.moe_w4_attend_decode(cache._c, heads, q.data_ptr(), q_stride, dim ** -0.5 if scale is None else scale,
                                      max_len, out.data_ptr(), out_stride, mw._ptr(lse), track, mw._ptr(weight_out),
@@ -332,7 +338,7 @@ def kv_evict(cache: PagedKVCache, seen, budget: int, sink: int = 0, recent: int 
     key = (budget, max_len)
     size = cache._sizes.get(key)
     if size is None:
-        size = cache._sizes[key] = max(mw.moe_w4_evict_workspace_size(cache._c, *key), mw.CTRL_BYTES)
+        size = cache._remember(key, mw.moe_w4_evict_workspace_size(cache._c, *key))
     ws = cache._workspace(size, stream, handle)
     status = mw.moe_w4_kv_evict(cache._c, cache._t, seen.data_ptr(), budget, sink, recent, max_len, lens_out.data_ptr(),
                                 weight_out.data_ptr(), pos_out.data_ptr(), ws[0], ws[1], handle)

@@ -160,3 +160,15 @@ def test_other_calls_refuse_numbers_past_32_bits(sv, calls):
     with pytest.raises(ValueError, match="top"):
         sv.token_logprobs(Fake((2, 100), torch.float32, "cuda:0"), top=2 ** 32 + 3)
     assert not calls
+
+
+def test_growing_sequences_leave_nothing_behind(sv, calls):
+    """A decode loop gives another bound every step: what the cache remembers of them does not grow."""
+    c = cache(sv, pages=4096)
+    q = Fake((2, 4, 64), torch.bfloat16, "cuda:0")
+    seen = Fake((2,), torch.int32, "cuda:0")
+    for n in range(1, 3000):
+        sv.attend_decode(c, q, max_len=n)
+        sv.kv_evict(c, seen, n, max_len=n + 1)
+    assert len(c._sizes) <= 256 and len(c._kept) <= 8
+    assert calls[-1][1][-2] >= sv.mw.moe_w4_evict_workspace_size(c._c, 2999, 3000)   # and the workspace still suffices
