@@ -9,11 +9,11 @@
 // without alternatives 86% of that time, the copies alone 71%).
 // Latency bounds small ones (1 x 32000 fp32: 7.5 us; 16 x 131072 bf16, top 20: 9.9).
 //
-// A row belongs to a cluster of 1 to 8 CTAs, each with a contiguous part; the
-// clusters of a resident grid take rows in turn.  A thread streams vectors of
-// 16 bytes through slots of shared memory that only it uses, so nothing but
-// its own copies is waited for, and the ring runs on into the next row while
-// the CTA finishes this one.  It keeps a reference maximum, Z and
+// Few rows: a row belongs to a cluster of 1 to 8 CTAs, each with a contiguous part.
+// More rows than fit at once: single smaller CTAs of a resident grid take rows in
+// turn.  A thread streams vectors of 16 bytes through slots of shared memory that
+// only it uses, so nothing but its own copies is waited for, and the ring runs on
+// into the CTA's next row while it finishes this one.  It keeps a reference maximum, Z and
 // U = sum e (x - m), and its largest logit.
 //
 // The top k of a part: the k-th largest of the threads' maxima is a lower bound
@@ -206,8 +206,8 @@ struct LpShared {
     float quarter_max[kLpQuarters][NT];
     uint16_t hits[kLpQuarters * NT];             // quarter and thread of the vectors to read again
     static constexpr int kCtas = NT == 256 ? kLpMaxCluster : 1;   // smaller CTAs come one to a row
-    uint64_t part_words[2][kCtas][32];           // of the cluster's CTAs, in CTA 0; by turns
-    float part_sums[2][kCtas][3];
+    uint64_t part_words[kCtas][32];              // of the cluster's CTAs, in CTA 0; a cluster has one row
+    float part_sums[kCtas][3];
     Sums sums[NT / 32];
     int warp_count[NT / 32];
     int count, hit_count;
@@ -445,8 +445,8 @@ __global__ void __launch_bounds__(NT, kLpPerSm / NT) token_logprobs_kernel(const
 #pragma unroll
     for (int i = 0; i < kLpStages; ++i) load(i);
 
-    int stage = 0, turn = 0;
-    for (int r = first; r < a.n; r += step, turn ^= 1) {
+    int stage = 0;
+    for (int r = first; r < a.n; r += step) {
         const Part<T, NT> p(a, r, rank, ctas);
         float scalar = -INFINITY;
         if (p.scalar >= 0) scalar = Logit<T>::one(p.row + p.scalar);
@@ -526,22 +526,22 @@ __global__ void __launch_bounds__(NT, kLpPerSm / NT) token_logprobs_kernel(const
         const int kk = min(a.top, p.count);
         if (kk) word = part_top(p, most, scalar, kk, sh);
         else __syncthreads();
-        if (NT == 256 && ctas > 1 && r == first) cluster_wait();
+        if (NT == 256 && ctas > 1) cluster_wait();
         if (warp == 0) {
             s = warp_join(lane < (NT / 32) ? sh.sums[lane] : Sums{-INFINITY, 0.f, 0.f});
             if (NT == 256 && ctas > 1) {
-                st_cluster(at_rank(&sh.part_words[turn][rank][lane], 0), word);
-                if (lane < 3) st_cluster(at_rank(&sh.part_sums[turn][rank][lane], 0), lane == 0 ? s.m : lane == 1 ? s.Z : s.U);
+                st_cluster(at_rank(&sh.part_words[rank][lane], 0), word);
+                if (lane < 3) st_cluster(at_rank(&sh.part_sums[rank][lane], 0), lane == 0 ? s.m : lane == 1 ? s.Z : s.U);
             }
         }
         if (NT == 256 && ctas > 1) cluster_sync();
         else __syncthreads();
         if (rank == 0 && warp == 0) {
             if (NT == 256 && ctas > 1) {
-                const float* q = sh.part_sums[turn][lane < ctas ? lane : 0];
+                const float* q = sh.part_sums[lane < ctas ? lane : 0];
                 s = warp_join(lane < ctas ? Sums{q[0], q[1], q[2]} : Sums{-INFINITY, 0.f, 0.f});
                 if (a.top)
-                    for (int c = 1; c < ctas; ++c) word = warp_merge(word, sh.part_words[turn][c][lane]);
+                    for (int c = 1; c < ctas; ++c) word = warp_merge(word, sh.part_words[c][lane]);
             }
             // a NaN, +inf (x - m is NaN then), or nothing but -inf
             const bool none = s.m == -INFINITY || isnan(s.Z);
@@ -607,7 +607,7 @@ static cudaError_t launch_logprobs(const LogprobArgs& a, cudaStream_t st) {
     }
     int ctas = 1;
     while (ctas < kLpMaxCluster && a.n * ctas * 2 <= places / 4 * 3 && vecs >= 256 * ctas * 2) ctas *= 2;
-    return launch_logprobs<T, 256>(a, ctas, a.n, dev, st);
+    return launch_logprobs<T, 256>(a, ctas, a.n, dev, st);   // one row a cluster
 }
 
 }  // namespace mw4
