@@ -34,11 +34,7 @@ def _need(ok, what):
         raise ValueError(what)
 
 
-def _int(n, what):
-    """A C int: ctypes would cut a larger number to 32 bits."""
-    if not -2 ** 31 <= n < 2 ** 31:
-        raise ValueError(what + ": a 32-bit integer")
-    return n
+_INT = 2 ** 31   # C ints: ctypes would cut larger numbers to 32 bits
 
 
 # The current stream's handle without the Stream object around it, where torch offers that (a call saves 3 us).
@@ -296,7 +292,9 @@ def attend_decode(cache: PagedKVCache, q, scale: Optional[float] = None, max_len
     if max_len is None:
         max_len = cache.capacity if track is None else min(cache.capacity, cache.weight.shape[2])
     else:
-        max_len = _int(int(max_len), "max_len")
+        max_len = int(max_len)
+    if not -_INT <= max_len < _INT:
+        raise ValueError("max_len: a 32-bit integer")
     handle = _handle(stream, device)
     key = (heads, max_len, weight_out is not None)
     size = cache._sizes.get(key)
@@ -332,8 +330,10 @@ def kv_evict(cache: PagedKVCache, seen, budget: int, sink: int = 0, recent: int 
         pos_out = cache.pos
     else:
         cache._check_like_weight(pos_out, torch.int32)
-    max_len = min(cache.capacity, cache.weight.shape[2]) if max_len is None else _int(int(max_len), "max_len")
-    budget, sink, recent = _int(int(budget), "budget"), _int(sink, "sink"), _int(recent, "recent")
+    max_len = min(cache.capacity, cache.weight.shape[2]) if max_len is None else int(max_len)
+    budget = int(budget)
+    if not (-_INT <= budget < _INT and -_INT <= sink < _INT and -_INT <= recent < _INT and -_INT <= max_len < _INT):
+        raise ValueError("budget, sink, recent and max_len: 32-bit integers")
     handle = _handle(stream, device)
     key = (budget, max_len)
     size = cache._sizes.get(key)
@@ -371,7 +371,8 @@ def token_logprobs(logits, targets=None, top: int = 0, stream=None) -> TokenLogp
     device = logits.device
     if targets is not None:
         _check_index(targets, n, device, "targets")
-    top = _int(top, "top")
+    if not -_INT <= top < _INT:
+        raise ValueError("top: a 32-bit integer")
     handle = _handle(stream, device)
     key = (device.index, handle)
     ws = _ctrl.get(key)
