@@ -13,14 +13,14 @@
 // its tokens are cut into tiles of 64.  The tiles of all rows, in order, form
 // one list that the CTAs of a resident grid share out in equal contiguous
 // parts, so mixed lengths balance without the host knowing them.  A row that
-// crosses CTAs leaves partial results (running maximum, sum, unnormalised
+// crosses CTAs leaves partial results (reference maximum, sum, unnormalised
 // output); at the end each of its CTAs waits for all of them (a cooperative
 // launch, bounded waits) and adds up its own share of the row's output in CTA
 // order, so that the join is spread over the CTAs too.
 //
 // Each warp is a pipeline of its own: it owns 16 tokens of every tile, keeps
 // their keys and values arriving through cp.async in a ring of its own (units
-// of 16 rows, across row ends), and holds its own running maximum, sum and
+// of 16 rows, across row ends), and holds its own reference maximum, sum and
 // output; warps meet only at row ends.
 //
 // Products are taken transposed, tokens (keys) or dimensions (values) as the 16
@@ -30,9 +30,10 @@
 // per 16 tokens of 256 dimensions, the tensor pipe is 11% busy, and loads are
 // what warps wait for.
 //
-// Measured (bf16, CUDA graph): 1 x 131,072 tokens, 2 kv heads of 256, group 8:
-// 47.8 us for 268 MB, 83% of the copy rate; 32 x 8192, 8 heads of 128, group 4:
-// 164 us for 1.07 GB, 96%.  A call's fixed cost is about 10 us: lengths and page
+// Measured (CUDA graph): 1 x 131,072 tokens, 2 kv heads of 256, group 8: 47.7 us for
+// 268 MB, 83% of the copy rate; 32 x 8192, 8 heads of 128, group 4: 165 us for
+// 1.07 GB, 96%; bf16 and fp16 alike.  Pages that are no multiple of 8 slots are copied
+// row by row (16 x 8192, 8 heads of 128: 101 us with a token a page, 88 with 16).  A call's fixed cost is about 10 us: lengths and page
 // numbers (3 us), the first units (1.5), a row's end (2), its join (3).
 #include <climits>
 
@@ -148,7 +149,11 @@ MW4_DEV uint32_t transpose8(uint32_t v) {
 MW4_DEV void cp_async_16_to(uint32_t dst, const void* src, uint64_t policy) {
     asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2;" :: "r"(dst), "l"(src), "l"(policy) : "memory");
 }
-// The cache is read once a call: it leaves L2 before what is used again.
+// Keys and values leave L2 before what is used again (1 x 131,072 tokens of 2 heads
+// of 256: 45.8 us, with the usual policy 48.8).  Most are read once a call; where head
+// blocks or sequences share them it does not hurt either (16 x 16384, 4 heads of 128,
+// group 48 in two blocks: 184.9 and 186.9; 16 sequences of 8192 with 7168 in common:
+// 57.3 and 57.8).
 MW4_DEV uint64_t read_once() {
     uint64_t p;
     asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));

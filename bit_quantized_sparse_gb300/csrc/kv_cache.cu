@@ -27,9 +27,11 @@ struct AppendArgs {
 constexpr int kAppendThreads = 256;
 
 // One thread per 16-byte piece of a (token, head) row: it copies that piece of
-// the key and of the value.  Latency bounds it: one chain of three loads (index,
-// page number, data) and a store (16 tokens: 2.4 us, 4096 tokens of 2 heads of
-// 256: 3.8 us for 17 MB, 65% of the copy rate).
+// the key and of the value.  Latency bounds it: four trips to memory one after the
+// other (sequence, index, page number, data; the data's address needs only the
+// token's number, but it is asked for when the place is known to be good) and a
+// store (16 tokens: 2.4 us, 4096 tokens of 2 heads of 256: 3.8 us for 17 MB, 65% of
+// the copy rate).
 __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const AppendArgs a) {
     griddep_wait();
     griddep_launch_dependents();   // the attention that follows may start to launch

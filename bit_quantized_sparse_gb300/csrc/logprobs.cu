@@ -7,7 +7,7 @@
 // exponential and about six instructions, and the warps wait about as much for
 // those as for the copies (4096 x 49999 fp16, top 5: 82 us, 73% of the copy rate;
 // without alternatives 86% of that time, the copies alone 71%).
-// Latency bounds small ones (1 x 32000 fp32: 7.5 us; 16 x 131072 bf16, top 20: 9.9).
+// Latency bounds small ones (1 x 32000 fp32: 7.9 us; 16 x 131072 bf16, top 20: 9.7).
 //
 // Few rows: a row belongs to a cluster of 1 to 8 CTAs, each with a contiguous part.
 // More rows than fit at once: single smaller CTAs of a resident grid take rows in
