@@ -66,11 +66,6 @@ struct Steps {
     static constexpr int HEADS = 8 * NB, QROW = D * 2, QCH = D / 8, QBYTES = HEADS * QROW;   // queries in shared memory
     static constexpr int PER = 32 / CH, COPIES = SUB / PER;     // rows of a warp-wide copy
     static constexpr int TURN = 8 / PER;                        // copies until the swizzle repeats
-    // Probabilities enter the product in 16 bits.  One bf16 term, or one fp16 term for an
-    // fp16 output, would cost as much accuracy as the output's rounding, so they get a
-    // second one for what the first leaves.  For codes with a bf16 output one fp16 term
-    // (2^-11) is an eighth of that rounding and 2^-7 of the codes' own.
-    static constexpr int TERMS = E8 && !std::is_same<T, __half>::value ? 1 : 2;
 
     // Where piece p of row r lies in its row: 8 consecutive rows' pieces share no bank.
     static MW4_DEV uint32_t swizzled(int p, int r) { return (p ^ (CH == 4 ? (r >> 1) & 3 : r & 7)) << 4; }
@@ -132,7 +127,10 @@ struct Steps {
 
     // ---- a warp's results of a row ----
     float o[NB][D / 16][4], m[NB][2], l[NB][2], ref, qs[NB][2];
-    uint32_t hi[NB][R][2], lo[NB][R][2];   // P^T of 16 tokens, 0..7 and 8..15: 16 bits, and what they leave
+    // P^T of 16 tokens, 0..7 and 8..15: 16 bits, and what they leave.  One term alone would be off by
+    // 2^-9 (bf16) or 2^-12 (fp16) of what the output is made of, and that shows where values cancel,
+    // whatever the output's own rounding.
+    uint32_t hi[NB][R][2], lo[NB][R][2];
     MW4_DEV void start(const float* sh_qs) {
 #pragma unroll
         for (int n = 0; n < NB; ++n) {
@@ -285,10 +283,8 @@ struct Steps {
                     const float w = E8 ? vs[r][x] * inv : 1.f, w0 = E8 ? p0 * w : p0, w1 = E8 ? p1 * w : p1;
                     const uint32_t h = Elem<P>::pack(w0, w1);
                     hi[n][r][x] = transpose8(h);
-                    if (TERMS == 2) {
-                        const float2 back = Elem<P>::unpack(h);
-                        lo[n][r][x] = transpose8(Elem<P>::pack(w0 - back.x, w1 - back.y));
-                    }
+                    const float2 back = Elem<P>::unpack(h);
+                    lo[n][r][x] = transpose8(Elem<P>::pack(w0 - back.x, w1 - back.y));
                 }
         }
     }
@@ -329,7 +325,7 @@ struct Steps {
 #pragma unroll
                     for (int n = 0; n < NB; ++n) {
                         Elem<P>::mma(o[n][jp * 2 + c], f[c], hi[n][r][0], hi[n][r][1]);
-                        if (TERMS == 2) Elem<P>::mma(o[n][jp * 2 + c], f[c], lo[n][r][0], lo[n][r][1]);
+                        Elem<P>::mma(o[n][jp * 2 + c], f[c], lo[n][r][0], lo[n][r][1]);
                     }
             }
     }
