@@ -27,11 +27,13 @@
 namespace mw4 {
 
 // Ring units per warp and CTAs per SM for a head size; NB blocks of 8 query heads.
-// Two blocks of heads of 128 over codes: with 3 CTAs an SM registers would spill, 96 bytes
-// (8 x 16,384 tokens, 4 kv heads of 128, group 16: 54.2 us, with 2 40.2, and with rings of
-// 5 units 40.7).
+// Over codes, two blocks of heads of 128 and three of 64: with 3 CTAs an SM registers would
+// spill, 96 and 300 bytes (8 x 16,384 tokens, 4 kv heads of 128, group 16: 54.2 us, with 2 40.2,
+// and with rings of 5 units 40.7; 16 x 8192, 4 of 64, group 24: 53.7, with 2 42.8).
 template <bool E8, int D, int NB> struct ListCfg;
-template <bool E8, int NB> struct ListCfg<E8, 64, NB> { static constexpr int slots = 5, ctas = NB == 1 ? 4 : 3; };
+template <bool E8, int NB> struct ListCfg<E8, 64, NB> {
+    static constexpr int slots = E8 && NB == 3 ? 8 : 5, ctas = NB == 1 ? 4 : E8 && NB == 3 ? 2 : 3;
+};
 template <bool E8, int NB> struct ListCfg<E8, 128, NB> { static constexpr int slots = 3, ctas = E8 && NB == 2 ? 2 : 3; };
 template <bool E8> struct ListCfg<E8, 128, 3> { static constexpr int slots = 5, ctas = 2; };
 template <bool E8, int NB> struct ListCfg<E8, 256, NB> { static constexpr int slots = 2, ctas = 2; };
@@ -43,7 +45,8 @@ __global__ void __launch_bounds__(kAttThreads, ListCfg<E8, D, NB>::ctas) attend_
     using St = Steps<T, E8, D, NB>;
     constexpr int HEADS = 8 * NB, SUB = St::SUB, TILE = SUB * kAttWarps, S = ListCfg<E8, D, NB>::slots;
     constexpr int UNIT = St::UNIT;
-    __shared__ float sh_m[kAttWarps][HEADS], sh_l[kAttWarps][HEADS], sh_qs[HEADS];
+    __shared__ float sh_m[kAttWarps][HEADS], sh_l[kAttWarps][HEADS];
+    __shared__ __align__(8) float sh_qs[HEADS];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     uint8_t* ring = smem + warp * S * UNIT;
     const uint32_t ring_u = smem_u32(ring), ring_end = ring_u + S * UNIT;
@@ -165,7 +168,7 @@ __global__ void __launch_bounds__(kAttThreads, ListCfg<E8, D, NB>::ctas) attend_
         heads = min(a.block_heads, a.group - hb * a.block_heads);
         head0 = kvh * a.group + hb * a.block_heads;
         first = at.tile;
-        st.start(sh_qs);
+        st.start();
     };
     // The end of a row's tiles here: the warps' results meet, brought to a common
     // maximum, outputs added in warp order through the unit that has just been used.
@@ -195,7 +198,7 @@ __global__ void __launch_bounds__(kAttThreads, ListCfg<E8, D, NB>::ctas) attend_
                 for (int w = 1; w < kAttWarps; ++w) M = fmaxf(M, sh_m[w][h]);
                 // a warp without a score above -inf: 0, or NaN where it has met one
                 const float f = st.m[n][c] == -INFINITY ? (st.l[n][c] == 0.f ? 0.f : NAN) : ex2(st.m[n][c] - M);
-                by[c] = E8 ? f * st.ref : f;
+                by[c] = f;
                 if (st.g == 0) sh_l[warp][h] = st.l[n][c] * f;
             }
             st.put(reinterpret_cast<float*>(ring + here), n, by[0], by[1]);
@@ -259,7 +262,7 @@ __global__ void __launch_bounds__(kAttThreads, ListCfg<E8, D, NB>::ctas) attend_
         cp_async_wait<S - 1>();
         __syncwarp();
         if (mine && !(u & 1))
-            st.keys(take, reinterpret_cast<const float*>(ring + (take - ring_u) + St::SCALES), q_u,
+            st.keys(take, reinterpret_cast<const float*>(ring + (take - ring_u) + St::SCALES), q_u, sh_qs,
                     !cut.all(at, t0) || loader.bad_pages, [&](int t) { return loader.gone(at, t0 + t); });
         else if (mine)
             st.values(take);

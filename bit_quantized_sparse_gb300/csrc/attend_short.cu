@@ -45,7 +45,7 @@ __global__ void __launch_bounds__(kAttThreads, ShortCfg<D, NB>::ctas) attend_sho
     constexpr int S = ShortCfg<D, NB>::slots, SUB = St::SUB, TILE = SUB * kAttWarps, UNIT = St::UNIT, HEADS = St::HEADS;
     extern __shared__ __align__(1024) uint8_t smem[];
     __shared__ float2 sh_ml[kAttWarps][HEADS];       // reference maximum (log2) and sum of each warp
-    __shared__ float sh_qs[HEADS];
+    __shared__ __align__(8) float sh_qs[HEADS];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int ctas = (int)cluster_size(), rank = (int)cluster_rank();
     uint8_t* ring = smem + warp * S * UNIT;
@@ -101,7 +101,7 @@ __global__ void __launch_bounds__(kAttThreads, ShortCfg<D, NB>::ctas) attend_sho
             fresh = false;
             St::store_q(qp, q_smem, sh_qs, a.scale_log2);
             __syncthreads();       // once in every warp, tiles or none
-            st.start(sh_qs);
+            st.start();
             if (tile >= p.tiles) break;
         }
         if (u >= 0) {
@@ -110,7 +110,7 @@ __global__ void __launch_bounds__(kAttThreads, ShortCfg<D, NB>::ctas) attend_sho
             const int t0 = token_of(tile) - (lane & (SUB - 1));
             if (cut.any(p, t0)) {
                 if (!(u & 1))
-                    st.keys(take, reinterpret_cast<const float*>(ring + (take - ring_u) + St::SCALES), q_u,
+                    st.keys(take, reinterpret_cast<const float*>(ring + (take - ring_u) + St::SCALES), q_u, sh_qs,
                             !cut.all(p, t0) || loader.bad_pages, [&](int t) { return loader.gone(p, t0 + t); });
                 else
                     st.values(take);
@@ -135,7 +135,7 @@ __global__ void __launch_bounds__(kAttThreads, ShortCfg<D, NB>::ctas) attend_sho
             for (int x = 4; x < 32; x <<= 1) st.l[i][c] += __shfl_xor_sync(0xffffffffu, st.l[i][c], x);
             if (st.g == 0) sh_ml[warp][i * 8 + 2 * st.t4 + c] = make_float2(st.m[i][c], st.l[i][c]);
         }
-        st.put(outs + i * 8 * (D + 4), i, E8 ? st.ref : 1.f, E8 ? st.ref : 1.f);
+        st.put(outs + i * 8 * (D + 4), i, 1.f, 1.f);
     }
     cluster_sync();
     // A warp in turn has up to 32 columns of four outputs of a head.  A lane works out

@@ -17,9 +17,22 @@
 
 namespace mw4 {
 
-// The reference of the values' scales lies so far above the largest that a larger
-// one seldom moves it; the product's terms keep 2^-35 of the row's largest.
-constexpr float kRefAbove = 8.f;
+// Over codes it is probabilities times the values' scales that enter a product, as sums of
+// two fp16 terms; and a token that takes nearly all the weight may have no value, or one of a
+// scale far from the others'.  So these have a reference of their own, the largest so far, which is
+// taken to 2^kTop and follows when one passes 2^(kTop + kRoom); it lies a whole power of two, of
+// -kReach to kReach, from the probabilities' own, which may be passed by 2^kGrow.  The second terms
+// are taken 2^kLower larger and added up apart: their smallest step is then 2^-36, so that one is off
+// by at most 2^-49 of the largest (2^-37 of 2^12, as scales are rounded up to powers of two).
+// Multiplying the codes by 2^-kLower instead, which fp16 holds as well, costs more (16 mixed
+// sequences of up to 32,768: 41.1 us, so 39.2, 38.6 without any of it).
+constexpr int kTop = 13, kRoom = 2, kLower = 12, kReach = 120, kGrow = 4;
+// Past this, fp32 scores are too coarse to tell by their sum with a scale's power whether a product has
+// outgrown its reference; differences are taken each time.
+constexpr float kCoarse = 262144.f;
+MW4_DEV float power2(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
+// log2 of a number that is not negative, rounded up (of 0 and what lies below 2^-126: -127, -126).
+MW4_DEV float exponent_up(float f) { return __uint_as_float(0x4b000000u | (__float_as_uint(f) + 0x7fffffu) >> 23) - (8388608.f + 127.f); }
 
 // 16 bytes of which `size`, 0 or 16, come from src and the others are zeros.
 MW4_DEV void cp_async_16_sized(uint32_t dst, const void* src, uint32_t size, uint64_t policy) {
@@ -125,13 +138,13 @@ struct Steps {
         }
     }
 
-    // ---- a warp's results of a row ----
-    float o[NB][D / 16][4], m[NB][2], l[NB][2], ref, qs[NB][2];
+    // ---- a warp's results of a row: outputs (over codes against 2^m / inv), references and sums ----
+    float o[NB][D / 16][4], m[NB][2], l[NB][2], inv[NB][2];
     // P^T of 16 tokens, 0..7 and 8..15: 16 bits, and what they leave.  One term alone would be off by
-    // 2^-9 (bf16) or 2^-12 (fp16) of what the output is made of, and that shows where values cancel,
+    // 2^-8 (bf16) or 2^-11 (fp16) of what the output is made of, and that shows where values cancel,
     // whatever the output's own rounding.
     uint32_t hi[NB][R][2], lo[NB][R][2];
-    MW4_DEV void start(const float* sh_qs) {
+    MW4_DEV void start() {
 #pragma unroll
         for (int n = 0; n < NB; ++n) {
 #pragma unroll
@@ -140,16 +153,15 @@ struct Steps {
             for (int c = 0; c < 2; ++c) {
                 m[n][c] = -INFINITY;
                 l[n][c] = 0.f;
-                qs[n][c] = sh_qs[n * 8 + 2 * t4 + c];
+                inv[n][c] = power2(kReach);
             }
         }
-        ref = 0.f;
     }
 
     // The tokens' keys: scores, the running maxima and sums, and the probabilities for the
     // values' product.  gone(t): token t of the unit takes no part.
     template <typename Gone>
-    MW4_DEV void keys(uint32_t unit, const float* scales, uint32_t q_u, bool some_gone, Gone gone) {
+    MW4_DEV void keys(uint32_t unit, const float* scales, uint32_t q_u, const float* sh_qs, bool some_gone, Gone gone) {
         float s[NB][R][4], odd[R][4];   // one block of heads: two chains of products each
 #pragma unroll
         for (int r = 0; r < R; ++r)
@@ -200,7 +212,13 @@ struct Steps {
             }
         }
         // s[n][r][2 x + c] becomes the score of token 16 r + 8 x + g with head 2 t4 + c
-        float vs[R][2];
+        float vs[R][2], qs[NB][2];     // (in registers all the while, heads' factors cost spills)
+#pragma unroll
+        for (int n = 0; n < NB; ++n) {
+            const float2 two = *reinterpret_cast<const float2*>(sh_qs + n * 8 + 2 * t4);
+            qs[n][0] = two.x;
+            qs[n][1] = two.y;
+        }
 #pragma unroll
         for (int r = 0; r < R; ++r)
 #pragma unroll
@@ -224,52 +242,31 @@ struct Steps {
                         for (int n = 0; n < NB; ++n) s[n][r][2 * x] = s[n][r][2 * x + 1] = -INFINITY;
                     }
         }
-        // The reference that the exponents are taken against follows the maximum only when
-        // that has grown by more than kLazy; that of the values' scales lies above the
-        // largest so far.
+        if constexpr (E8) weigh_codes(s, vs);
+        else weigh(s);
+    }
+
+    // The probabilities of 16-bit values from scores.  The reference that exponents are taken
+    // against follows the maximum only when that has grown by more than kLazy.
+    MW4_DEV void weigh(const float (&s)[NB][R][4]) {
         bool grow = false;
 #pragma unroll
-        for (int r = 0; r < R; ++r)
+        for (int n = 0; n < NB; ++n)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                if (E8) grow |= vs[r][e >> 1] > ref;
+            for (int r = 0; r < R; ++r)
 #pragma unroll
-                for (int n = 0; n < NB; ++n) grow |= s[n][r][e] > m[n][e & 1] + (Elem<P>::kBelow + Elem<P>::kLazy);
-            }
+                for (int e = 0; e < 4; ++e) grow |= s[n][r][e] > m[n][e & 1] + (Elem<P>::kBelow + Elem<P>::kLazy);
         if (__any_sync(0xffffffffu, grow)) {
-            float fr = 1.f;
-            if (E8) {
-                float most = fmaxf(vs[0][0], vs[0][1]);
-                if (R > 1) most = fmaxf(most, fmaxf(vs[R - 1][0], vs[R - 1][1]));
-#pragma unroll
-                for (int x = 4; x < 32; x <<= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, x));
-                if (most > ref) {
-                    const float to = most * kRefAbove;
-                    fr = ref / to;
-                    ref = to;
-                }
-            }
 #pragma unroll
             for (int n = 0; n < NB; ++n)
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
-                    float to = fmaxf(s[n][0][c], s[n][0][c + 2]);
-                    if (R > 1) to = fmaxf(to, fmaxf(s[n][R - 1][c], s[n][R - 1][c + 2]));
-                    to = fmaxf(m[n][c], to - Elem<P>::kBelow);
-#pragma unroll
-                    for (int x = 4; x < 32; x <<= 1) to = fmaxf(to, __shfl_xor_sync(0xffffffffu, to, x));
+                    const float to = warp_most(fmaxf(m[n][c], most(s[n], c) - Elem<P>::kBelow));
                     const float f = m[n][c] == -INFINITY ? 0.f : ex2(m[n][c] - to);
                     m[n][c] = to;
-                    l[n][c] *= f;
-                    const float fo = E8 ? f * fr : f;
-#pragma unroll
-                    for (int j = 0; j < D / 16; ++j) {
-                        o[n][j][c] *= fo;
-                        o[n][j][c + 2] *= fo;
-                    }
+                    rescale(n, c, f, f);
                 }
         }
-        const float inv = E8 && ref > 0.f ? 1.f / ref : 0.f;
 #pragma unroll
         for (int n = 0; n < NB; ++n) {
             const float r0 = m[n][0] == -INFINITY ? 0.f : m[n][0], r1 = m[n][1] == -INFINITY ? 0.f : m[n][1];
@@ -280,12 +277,94 @@ struct Steps {
                     const float p0 = ex2(s[n][r][2 * x] - r0), p1 = ex2(s[n][r][2 * x + 1] - r1);
                     l[n][0] += p0;
                     l[n][1] += p1;
-                    const float w = E8 ? vs[r][x] * inv : 1.f, w0 = E8 ? p0 * w : p0, w1 = E8 ? p1 * w : p1;
+                    const uint32_t h = Elem<P>::pack(p0, p1);
+                    hi[n][r][x] = transpose8(h);
+                    const float2 back = Elem<P>::unpack(h);
+                    lo[n][r][x] = transpose8(Elem<P>::pack(p0 - back.x, p1 - back.y));
+                }
+        }
+    }
+
+    // Those over codes, from scores and the values' scales: against 2^m, and times a scale against
+    // 2^m / inv.
+    MW4_DEV void weigh_codes(const float (&s)[NB][R][4], const float (&vs)[R][2]) {
+        float lv[R][2];
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+            for (int x = 0; x < 2; ++x) lv[r][x] = exponent_up(vs[r][x]);
+        bool grow = false;
+#pragma unroll
+        for (int n = 0; n < NB; ++n)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                const float top_p = m[n][c] + kGrow, top_w = m[n][c] - exponent_up(inv[n][c]) + (kTop + kRoom);
+                grow |= fabsf(m[n][c]) > kCoarse;
+#pragma unroll
+                for (int r = 0; r < R; ++r)
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        grow |= s[n][r][2 * x + c] > top_p;
+                        grow |= s[n][r][2 * x + c] + lv[r][x] > top_w;
+                    }
+            }
+        if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+            for (int n = 0; n < NB; ++n)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    // by whole powers of two, so that the products' reference can stay where it is
+                    const bool none = m[n][c] == -INFINITY;
+                    const float high = warp_most(most(s[n], c)), to = none ? high : m[n][c] + fmaxf(0.f, ceilf(high - m[n][c]));
+                    float top = -INFINITY;
+#pragma unroll
+                    for (int r = 0; r < R; ++r)
+#pragma unroll
+                        for (int x = 0; x < 2; ++x) top = fmaxf(top, s[n][r][2 * x + c] - to + lv[r][x]);
+                    // (fminf and fmaxf let go of a NaN, as of infinite scores)
+                    const float by = none ? -INFINITY : m[n][c] - to, before = -exponent_up(inv[n][c]);
+                    const float least = fmaxf(ceilf(warp_most(top)) - kTop, (float)-kReach);
+                    const float now = fminf(fmaxf(rintf(before + by), least), (float)kReach);
+                    m[n][c] = to;
+                    inv[n][c] = power2(-(int)now);
+                    rescale(n, c, ex2(by), ex2(by + (before - now)));
+                }
+        }
+#pragma unroll
+        for (int n = 0; n < NB; ++n) {
+            const float r0 = fmaxf(m[n][0], -FLT_MAX), r1 = fmaxf(m[n][1], -FLT_MAX);   // (of -inf: every score is)
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    const float p0 = ex2(s[n][r][2 * x] - r0), p1 = ex2(s[n][r][2 * x + 1] - r1);
+                    l[n][0] += p0;
+                    l[n][1] += p1;
+                    // (the scale last: one that is large meets a small inv or a probability of 0)
+                    const float w0 = p0 * inv[n][0] * vs[r][x], w1 = p1 * inv[n][1] * vs[r][x];
                     const uint32_t h = Elem<P>::pack(w0, w1);
                     hi[n][r][x] = transpose8(h);
                     const float2 back = Elem<P>::unpack(h);
-                    lo[n][r][x] = transpose8(Elem<P>::pack(w0 - back.x, w1 - back.y));
+                    lo[n][r][x] = transpose8(Elem<P>::pack((w0 - back.x) * (1 << kLower), (w1 - back.y) * (1 << kLower)));
                 }
+        }
+    }
+    // This lane's largest score with head c of a block's two; the largest of lanes with the same heads.
+    static MW4_DEV float most(const float (&s)[R][4], int c) {
+        const float v = fmaxf(s[0][c], s[0][c + 2]);
+        return R > 1 ? fmaxf(v, fmaxf(s[R - 1][c], s[R - 1][c + 2])) : v;
+    }
+    static MW4_DEV float warp_most(float v) {
+#pragma unroll
+        for (int x = 4; x < 32; x <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, x));
+        return v;
+    }
+    MW4_DEV void rescale(int n, int c, float sums, float outputs) {
+        l[n][c] *= sums;
+#pragma unroll
+        for (int j = 0; j < D / 16; ++j) {
+            o[n][j][c] *= outputs;
+            o[n][j][c + 2] *= outputs;
         }
     }
 
@@ -293,45 +372,52 @@ struct Steps {
     // two tokens; exchanged to pairs of tokens they are rows g and g + 8, so row g of a product is
     // dimension 2 g of its 16 and row g + 8 dimension 2 g + 1.  Of 16-bit values they are g and g + 8.
     MW4_DEV void values(uint32_t unit) {
-#pragma unroll
-        for (int r = 0; r < R; ++r)
+        if constexpr (E8) {
 #pragma unroll
             for (int jp = 0; jp < D / 32; ++jp) {
-                uint32_t f[2][4];
-                if (E8) {
-                    uint32_t v[4];
-                    ldsm4_t(v, unit + at[jp & (CH >= 8 ? 3 : 1)] + (jp >> 2) * 128 + r * 16 * ROW);
+                uint32_t v[R][4];
 #pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        const uint32_t x = __byte_perm(v[2 * c], 0, 0x3120), y = __byte_perm(v[2 * c + 1], 0, 0x3120);
-                        f[c][0] = f16x2_of_codes((uint16_t)x);
-                        f[c][1] = f16x2_of_codes((uint16_t)(x >> 16));
-                        f[c][2] = f16x2_of_codes((uint16_t)y);
-                        f[c][3] = f16x2_of_codes((uint16_t)(y >> 16));
-                    }
-                } else {
+                for (int r = 0; r < R; ++r) ldsm4_t(v[r], unit + at[jp & (CH >= 8 ? 3 : 1)] + (jp >> 2) * 128 + r * 16 * ROW);
 #pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        uint32_t v[4];
-                        ldsm4_t(v, unit + at[(jp * 2 + c) & 3] + ((jp * 2 + c) >> 2) * 128 + r * 16 * ROW);
-                        f[c][0] = v[0];
-                        f[c][1] = v[2];
-                        f[c][2] = v[1];
-                        f[c][3] = v[3];
+                for (int c = 0; c < 2; ++c) {
+                    float low[NB][4];      // of the second terms
+#pragma unroll
+                    for (int r = 0; r < R; ++r) {
+                        const uint32_t x = __byte_perm(v[r][2 * c], 0, 0x3120), y = __byte_perm(v[r][2 * c + 1], 0, 0x3120);
+                        const uint32_t f[4] = {f16x2_of_codes((uint16_t)x), f16x2_of_codes((uint16_t)(x >> 16)),
+                                               f16x2_of_codes((uint16_t)y), f16x2_of_codes((uint16_t)(y >> 16))};
+#pragma unroll
+                        for (int n = 0; n < NB; ++n) {
+                            if (r == 0) low[n][0] = low[n][1] = low[n][2] = low[n][3] = 0.f;
+                            Elem<P>::mma(o[n][jp * 2 + c], f, hi[n][r][0], hi[n][r][1]);
+                            Elem<P>::mma(low[n], f, lo[n][r][0], lo[n][r][1]);
+                        }
                     }
+#pragma unroll
+                    for (int n = 0; n < NB; ++n)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) o[n][jp * 2 + c][e] = fmaf(low[n][e], 1.f / (1 << kLower), o[n][jp * 2 + c][e]);
                 }
+            }
+        } else {
 #pragma unroll
-                for (int c = 0; c < 2; ++c)
+            for (int jp = 0; jp < D / 32; ++jp)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    uint32_t v[4];
+                    ldsm4_t(v, unit + at[(jp * 2 + c) & 3] + ((jp * 2 + c) >> 2) * 128);
+                    const uint32_t f[4] = {v[0], v[2], v[1], v[3]};
 #pragma unroll
                     for (int n = 0; n < NB; ++n) {
-                        Elem<P>::mma(o[n][jp * 2 + c], f[c], hi[n][r][0], hi[n][r][1]);
-                        Elem<P>::mma(o[n][jp * 2 + c], f[c], lo[n][r][0], lo[n][r][1]);
+                        Elem<P>::mma(o[n][jp * 2 + c], f, hi[n][0][0], hi[n][0][1]);
+                        Elem<P>::mma(o[n][jp * 2 + c], f, lo[n][0][0], lo[n][0][1]);
                     }
-            }
+                }
+        }
     }
 
     // The outputs of block n of heads into [8][D + 4] floats, whose pitch meets no bank
-    // twice; by: factors of heads 2 t4 and 2 t4 + 1.
+    // twice, brought to m and then by factors of heads 2 t4 and 2 t4 + 1.
     MW4_DEV void put(float* buf, int n, float by0, float by1) const {
         buf += 2 * t4 * (D + 4) + (E8 ? 2 * g : g);
 #pragma unroll
@@ -339,8 +425,9 @@ struct Steps {
 #pragma unroll
             for (int j = 0; j < D / 16; ++j) {
                 const float by = c ? by1 : by0;
-                if (E8) {
-                    *reinterpret_cast<float2*>(buf + c * (D + 4) + j * 16) = make_float2(o[n][j][c] * by, o[n][j][c + 2] * by);
+                if (E8) {   // (one after the other: their product may be too small for what o * both is not)
+                    const float back = __uint_as_float((254u << 23) - __float_as_uint(inv[n][c]));
+                    *reinterpret_cast<float2*>(buf + c * (D + 4) + j * 16) = make_float2(o[n][j][c] * by * back, o[n][j][c + 2] * by * back);
                 } else {
                     buf[c * (D + 4) + j * 16] = o[n][j][c] * by;
                     buf[c * (D + 4) + j * 16 + 8] = o[n][j][c + 2] * by;

@@ -115,10 +115,11 @@ int moe_w4_kv_read(const moe_w4_kv_cache* c, const moe_w4_kv_tokens* t, cudaStre
  * anything.  Scales of tokens that are seen are finite and not negative.  Sums are fp32:
  * of bf16 codes, values are below 2^80 in magnitude, and so is `scale` times a head's
  * largest query times a key's scale.
- * Queries enter the product as fp16, scaled by a power of two per head so that
+ * Over codes, queries enter the product as fp16, scaled by a power of two per head so that
  * the largest is 2^14 to 2^15: exact, but for those below 2^-29 of the largest,
  * which are off by at most 2^-39 of it.  Probabilities times the values' scales are two fp16
- * terms, off by at most 2^-21, or 2^-35 of the row's largest.
+ * terms, off by at most 2^-21, or 2^-49 of the row's largest such product (2^-157 where scales
+ * lie below 2^-100).  Probabilities below 2^-125 of the row's largest count as 0.
  * The workspace of moe_w4_attend_window is moe_w4_attend_workspace_size(..., 0)
  * bytes.  Members as the arguments of
  * moe_w4_attend_decode. */
