@@ -16,14 +16,16 @@
 // and sines of a batch's tokens are worked out once a CTA, in shared memory, while
 // the batch's rows arrive.
 //
-// 4096 tokens of 18 heads of 256, 64 of them turning: 15.4 us for 75 MB (a copy of
-// them takes 12.3); 2501 tokens of 40 heads of 128: 11.8; 16 tokens: 1.9.  Slower:
+// 4096 tokens of 18 heads of 256, 64 of them turning: 15.9 us for 75 MB (a copy of
+// them takes 12.3); 2501 tokens of 40 heads of 128: 12.4; 16 tokens: 1.9.  Slower:
 // the batch after asked for before this one is worked on (29; registers cost a CTA),
 // a warp for all of a token's heads and its angles in registers (16.3, 15.0 and 2.2).
 //
 // An angle is positions * turns modulo 2^64: the product's high 32 bits are the
 // fraction of a turn, so that no position, however far, loses bits to a range
-// reduction (with an fp32 angle 131,071 * 1 rad is off by 2^-8 rad).
+// reduction (with an fp32 angle 131,071 * 1 rad is off by 2^-8 rad).  Cosine and sine are
+// those of half turns, to two steps of fp32; the fast ones (15.5 and 11.8 us) are off by
+// 2^-21, which shows where a result is small.
 #include "serving.cuh"
 #include "moe_w4_longctx.h"
 
@@ -133,10 +135,10 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas) qk_norm_rope_kernel(c
             const int axis = a.axis ? max(0, min(a.axis[p], a.axes - 1)) : 0;
             const int pos = a.positions[axis * a.pos_stride + min(t, a.n - 1)];
             const uint64_t turned = (uint64_t)(int64_t)pos * a.turns[p];
-            const float angle = (float)(int32_t)(turned >> 32) * (float)(3.14159265358979323846 / 2147483648.0);   // -pi .. pi
-            float* to = turn + 2 * (e - p) + p;
-            to[0] = __cosf(angle) * a.scale;
-            to[a.pairs] = __sinf(angle) * a.scale;
+            float* to = turn + 2 * (e - p) + p, sine, cosine;
+            sincospif((float)(int32_t)(turned >> 32) * (1.f / 2147483648.f), &sine, &cosine);   // of -1 .. 1 half turns
+            to[0] = cosine * a.scale;
+            to[a.pairs] = sine * a.scale;
         }
         __syncthreads();                               // (the other table is free: everybody is past its last use)
         const float* cs = turn + 2 * (token - token0) * a.pairs + 4 * lane;

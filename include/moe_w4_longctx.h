@@ -36,7 +36,8 @@ typedef struct {
 
 /* Per head of n tokens, queries and keys alike:
  *   y = x * rsqrt(mean(x^2) + eps) * w      (w + 1 with unit_offset)
- * and then the rotation of y; all in fp32, rounded once.
+ * and then the rotation of y; all in fp32 (cosines and sines are off by at most 2^-22),
+ * rounded once.
  *   dtype     bf16 or fp16, of q, k, outputs and weights; head_dim 64, 128 or 256
  *   q, q_out  [n][n_q_heads][head_dim], tokens q_stride (qo_stride) elements
  *             apart, multiples of 8; 16-byte aligned; k alike, n_k_heads may be 0
