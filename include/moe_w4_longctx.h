@@ -104,7 +104,8 @@ int moe_w4_kv8_append(const moe_w4_kv8_cache* c, const moe_w4_kv_tokens* t, cuda
 
 /* Reads tokens back, rounded once from code * scale; they may be named in any order
  * and more than once.  A token that the cache does not have is zeros (and sets
- * MOE_W4_STATUS_BAD_INDEX, unless it is the last one of a sequence of length 0).
+ * MOE_W4_STATUS_BAD_INDEX, unless it is the last one of a sequence of length 0);
+ * a cache of 0 sequences has none.
  * moe_w4_kv_read does the same for a cache of 16-bit values. */
 int moe_w4_kv8_read(const moe_w4_kv8_cache* c, const moe_w4_kv_tokens* t, cudaStream_t stream);
 int moe_w4_kv_read(const moe_w4_kv_cache* c, const moe_w4_kv_tokens* t, cudaStream_t stream);
