@@ -5,8 +5,9 @@ compiled in parallel, then linked).  Run as `python -m bit_quantized_sparse_gb30
 sources with MW4_DEBUG_CHECKS defined, which adds device-side bounds checks on
 every index the kernels read from the routing records (positions, block
 records, units); a failed check sets MOE_W4_STATUS_BAD_INDEX in the status
-word and the access is clamped into range instead of made.  The binding loads
-it when the environment has MOE_W4_DEBUG=1."""
+word and the access is clamped into range instead of made.  It also refuses an
+append of 8-bit codes whose rows have a wrong order.  The binding loads it when
+the environment has MOE_W4_DEBUG=1."""
 import concurrent.futures
 import os
 import shutil

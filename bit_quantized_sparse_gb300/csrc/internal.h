@@ -69,6 +69,8 @@ constexpr int kCtrlEpochWord = 61;
 // while it is non-zero, the T=1 kernel's CTA 0 does not publish its router
 // scores, so every routed CTA's bounded wait for them runs out.
 constexpr int kCtrlInjectWord = 60;
+// Word of pad[] in which a debug build keeps whether an append of codes is refused for its rows' order.
+constexpr int kCtrlDisorderWord = 59;
 constexpr int kDownReuseMaxI = 512;
 inline int down_blocks_per_unit(int I) { return I <= kDownReuseMaxI ? kDownBlocksPerUnit : 1; }
 // Smallest token block the grouping may use (a tile override); sizes the block records.

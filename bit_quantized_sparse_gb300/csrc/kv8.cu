@@ -35,6 +35,7 @@ struct Append8Args {
     const int32_t* slot;
     int n, window, windows;   // rows; of a window; windows
     unsigned int* status;
+    unsigned int* disorder;   // debug builds: not 0 where the rows' order is wrong
 };
 
 constexpr int kSingleThreads = 256, kRowsThreads = 128, kLongThreads = 256;
@@ -89,6 +90,40 @@ MW4_DEV void row_at(const Append8Args& a, int i, int& b, int& t) {
     if (a.slot && t == -1) t = -2;
 }
 
+// Debug builds: a block whose tokens are not consecutive rows would be several runs', each with its
+// own scale.  Whether there is one costs a look at all rows from each, so the product does not ask; here
+// such a call writes nothing.
+MW4_DEV bool refused(const Append8Args& a) {
+#ifdef MW4_DEBUG_CHECKS
+    return *a.disorder;
+#else
+    (void)a;
+    return false;
+#endif
+}
+#ifdef MW4_DEBUG_CHECKS
+__global__ void kv8_append_order_kernel(const Append8Args a) {
+    const int i = (int)(blockIdx.x * blockDim.x + threadIdx.x);
+    if (i >= a.n) return;
+    int b, t, ob, ot;
+    row_at(a, i, b, t);
+    if ((unsigned)b >= (unsigned)a.c.n_seqs || t < 0) return;
+    const int in_block = t & ((1 << a.s.shift) - 1);
+    if (i > 0 && in_block > 0) {
+        row_at(a, i - 1, ob, ot);
+        if (ob == b && ot == t - 1) return;                // not a run's first
+    }
+    for (int j = 0; j < i; ++j) {
+        row_at(a, j, ob, ot);
+        if (ob == b && ot >= 0 && ot >> a.s.shift == t >> a.s.shift) {
+            raise_status(a.status, MOE_W4_STATUS_BAD_INDEX);
+            *a.disorder = 1;
+            return;
+        }
+    }
+}
+#endif
+
 // The exponent of the smallest power of two that brings `top` to 448 = 1.75 * 2^8 or below.
 MW4_DEV int scale_exponent(float top) {
     const uint32_t u = __float_as_uint(top);
@@ -142,6 +177,7 @@ __global__ void __launch_bounds__(kSingleThreads) kv8_append_single_kernel(const
                                                                           uint64_t per_piece, FastDiv per_head) {
     griddep_wait();
     griddep_launch_dependents();
+    if (refused(a)) return;
     const int64_t at = (int64_t)blockIdx.x * kSingleThreads + threadIdx.x;
     const uint64_t token = __umul64hi((uint64_t)at, per_piece);
     const bool on = token < (uint64_t)a.n;                 // a head's lanes agree
@@ -333,6 +369,7 @@ template <typename T, int D>
 __global__ void __launch_bounds__(kRowsThreads, rows_warps(D) * 32 / kRowsThreads) kv8_append_rows_kernel(const Append8Args a) {
     griddep_wait();
     griddep_launch_dependents();
+    if (refused(a)) return;
     const int64_t item = (int64_t)blockIdx.x * (kRowsThreads / 32) + (threadIdx.x >> 5);
     const int per_window = 2 * a.c.n_kv_heads;
     const int w = (int)(item / per_window), hv = (int)(item - (int64_t)w * per_window);
@@ -362,6 +399,7 @@ __global__ void __launch_bounds__(kLongThreads, long_ctas(D)) kv8_append_long_ke
     __shared__ int sh_found[WARPS];
     griddep_wait();
     griddep_launch_dependents();
+    if (refused(a)) return;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int per_window = 2 * a.c.n_kv_heads;
     const int w = blockIdx.x / per_window, hv = blockIdx.x - w * per_window;
@@ -469,6 +507,14 @@ template <typename T>
 static cudaError_t launch_append8(const Append8Args& a, int dim, cudaStream_t st) {
     const int sms = sm_count();
     if (sms < 1) return cudaErrorInvalidDevice;
+#ifdef MW4_DEBUG_CHECKS
+    cudaError_t e = cudaMemsetAsync(a.disorder, 0, sizeof(*a.disorder), st);
+    if (e == cudaSuccess) {
+        kv8_append_order_kernel<<<(unsigned)((a.n - 1) / 256 + 1), 256, 0, st>>>(a);
+        e = cudaGetLastError();
+    }
+    if (e != cudaSuccess) return e;
+#endif
     if (a.s.shift == 0) return launch_append8_single<T>(a, dim, st);
     return dim == 64 ? launch_append8_rows<T, 64>(a, sms, st)
            : dim == 128 ? launch_append8_rows<T, 128>(a, sms, st) : launch_append8_rows<T, 256>(a, sms, st);
@@ -626,6 +672,7 @@ int moe_w4_kv8_append(const moe_w4_kv8_cache* c, const moe_w4_kv_tokens* t, cuda
     a.slot = t->slot;
     a.n = t->n;
     a.status = &static_cast<Ctrl*>(t->workspace)->status;
+    a.disorder = &static_cast<Ctrl*>(t->workspace)->pad[kCtrlDisorderWord];
     return launched(c->c.dtype == MOE_W4_TYPE_BF16 ? launch_append8<__nv_bfloat16>(a, c->c.head_dim, stream)
                                                    : launch_append8<__half>(a, c->c.head_dim, stream));
 }

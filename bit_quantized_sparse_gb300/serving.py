@@ -315,7 +315,9 @@ def kv_append(cache: PagedKVCache, k, v, seq=None, slot=None, pos=None, stream=N
                starts the token's weight at 0
 
     Into a PagedKVCache8 they go as codes with a scale for each block of tokens (moe_w4_kv8_append says how it is
-    chosen): the tokens of a block are consecutive rows with consecutive indexes, and `pos` is not taken.
+    chosen), and `pos` is not taken.  There the tokens of a block have to be consecutive rows with consecutive indexes:
+    sequence after sequence, not step after step.  Otherwise the block's scale is not defined; the kernels do not ask
+    (those of the debug build do, and set the status).
     """
     if cache._c8 is not None:
         _need(pos is None, "pos: a cache of 8-bit codes keeps no positions")

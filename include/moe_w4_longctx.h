@@ -89,7 +89,10 @@ typedef struct {
 } moe_w4_kv_tokens;
 
 /* Writes tokens.  The tokens of one block have to be consecutive rows with
- * consecutive indexes.
+ * consecutive indexes (unlike rows of moe_w4_kv_append, which may have any order), and
+ * no token may be named twice: several rows of a block apart from one another each set
+ * its scale, and which one stays is not defined.  The debug build refuses such a call on the
+ * device: MOE_W4_STATUS_BAD_INDEX, nothing is written.
  * A block's scale is the smallest power of two, 2^-100 to 2^119, that brings the
  * largest finite magnitude of its tokens to 448 or below; codes are the nearest
  * (ties to even), infinities become +-448, NaN stays NaN.  Powers of two lose no
