@@ -18,6 +18,9 @@ and set the sticky status word (`PagedKVCache.status` and `reset`,
 `logprobs_status` and `logprobs_reset`).  For use in a CUDA graph make one call
 of the same sizes on the capturing stream first, so that its workspace exists
 (RuntimeError otherwise); the cache keeps every workspace that a graph may hold.
+A stream's calls and the graphs captured on it share its workspace: they run one
+after the other.  Graphs that are to run at once are captured on streams of their
+own.
 """
 from __future__ import annotations
 
