@@ -30,7 +30,6 @@ constexpr int kTop = 13, kRoom = 2, kLower = 12, kReach = 120, kGrow = 4;
 // Past this, fp32 scores are too coarse to tell by their sum with a scale's power whether a product has
 // outgrown its reference; differences are taken each time.
 constexpr float kCoarse = 262144.f;
-MW4_DEV float power2(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
 // log2 of a number that is not negative, rounded up (of 0 and what lies below 2^-126: -127, -126).
 MW4_DEV float exponent_up(float f) { return __uint_as_float(0x4b000000u | (__float_as_uint(f) + 0x7fffffu) >> 23) - (8388608.f + 127.f); }
 

@@ -49,12 +49,6 @@ MW4_DEV uint64_t ld_tagged(const uint64_t* p) {
 MW4_DEV uint32_t tag_of(uint64_t w) { return (uint32_t)(w >> 32); }
 MW4_DEV float val_of(uint64_t w) { return __uint_as_float((uint32_t)w); }
 
-MW4_DEV unsigned int atomic_add_acq_rel_gpu(unsigned int* p, unsigned int v) {
-    unsigned int old;
-    asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], %2;" : "=r"(old) : "l"(p), "r"(v) : "memory");
-    return old;
-}
-
 MW4_DEV void raise_status(unsigned int* status, unsigned int bits) {
     if (status) atomicOr(status, bits);
 }

@@ -45,10 +45,6 @@ constexpr int rows_warps(int dim) { return dim == 64 ? 32 : dim == 128 ? 24 : 16
 constexpr int long_ctas(int dim) { return dim == 64 ? 4 : dim == 128 ? 3 : 2; }
 constexpr int kLowest = -100, kHighest = 119;   // exponents of scales
 
-template <typename T> MW4_DEV float2 two_of(uint32_t u);
-template <> MW4_DEV float2 two_of<__nv_bfloat16>(uint32_t u) { return __bfloat1622float2(*reinterpret_cast<__nv_bfloat162*>(&u)); }
-template <> MW4_DEV float2 two_of<__half>(uint32_t u) { return __half22float2(*reinterpret_cast<__half2*>(&u)); }
-
 template <typename T> constexpr uint32_t kInfinite = std::is_same<T, __half>::value ? 0x7c00u : 0x7f80u;
 
 // The bits of the largest finite magnitude of N times 8 values: they order like numbers,
@@ -130,26 +126,24 @@ MW4_DEV int scale_exponent(float top) {
     const int e = (int)(u >> 23) - 127 - 8 + ((u & 0x7fffffu) > 0x600000u);
     return max(kLowest, min(kHighest, e));   // (zero and subnormals lie below)
 }
-MW4_DEV float power(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
 
 template <typename T>
 MW4_DEV uint2 codes8(const uint4& x, float inv) {
-    const float2 a = two_of<T>(x.x), b = two_of<T>(x.y), c = two_of<T>(x.z), d = two_of<T>(x.w);
+    const float2 a = Pair16<T>::unpack(x.x), b = Pair16<T>::unpack(x.y), c = Pair16<T>::unpack(x.z), d = Pair16<T>::unpack(x.w);
     return make_uint2(codes_of(a.x * inv, a.y * inv) | codes_of(b.x * inv, b.y * inv) << 16,
                       codes_of(c.x * inv, c.y * inv) | codes_of(d.x * inv, d.y * inv) << 16);
 }
 
 // Two codes brought to a scale `ratio` times smaller.
 MW4_DEV uint32_t recode(uint32_t two, float ratio) {
-    const uint32_t h = f16x2_of_codes((uint16_t)two);
-    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+    const float2 f = Pair16<__half>::unpack(f16x2_of_codes((uint16_t)two));
     return codes_of(f.x * ratio, f.y * ratio);
 }
 
 // The exponent that a block's scale has, the scale made a power of two: up to the next
 // where it is none, and one that is not positive and finite counts as the lowest.
 MW4_DEV int exponent_of(float& before) {
-    if (!(before > 0.f && before < INFINITY)) before = power(kLowest);
+    if (!(before > 0.f && before < INFINITY)) before = power2(kLowest);
     const uint32_t u = __float_as_uint(before);
     return max(kLowest, min(kHighest, (int)(u >> 23) - 127 + ((u & 0x7fffffu) != 0)));
 }
@@ -202,14 +196,14 @@ __global__ void __launch_bounds__(kSingleThreads) kv8_append_single_kernel(const
     uint32_t top = largest_finite<T>(kx) | largest_finite<T>(vx) << 16;
     for (int x = chunks >> 1; x; x >>= 1) top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, x));
     if (!there) return;
-    const int ke = scale_exponent(two_of<T>(top & 0xffffu).x), ve = scale_exponent(two_of<T>(top >> 16).x);
+    const int ke = scale_exponent(Pair16<T>::unpack(top & 0xffffu).x), ve = scale_exponent(Pair16<T>::unpack(top >> 16).x);
     const int64_t to = page * a.c.page_stride + in_page * a.c.slot_stride + h * a.c.head_stride + piece * 8;
-    *reinterpret_cast<uint2*>(reinterpret_cast<uint8_t*>(const_cast<uint16_t*>(a.c.k)) + to) = codes8<T>(kx, power(-ke));
-    *reinterpret_cast<uint2*>(reinterpret_cast<uint8_t*>(const_cast<uint16_t*>(a.c.v)) + to) = codes8<T>(vx, power(-ve));
+    *reinterpret_cast<uint2*>(reinterpret_cast<uint8_t*>(const_cast<uint16_t*>(a.c.k)) + to) = codes8<T>(kx, power2(-ke));
+    *reinterpret_cast<uint2*>(reinterpret_cast<uint8_t*>(const_cast<uint16_t*>(a.c.v)) + to) = codes8<T>(vx, power2(-ve));
     if (piece == 0) {
         const int64_t e = page * a.s.page_stride + h * a.s.head_stride + in_page;
-        a.s.k[e] = power(ke);
-        a.s.v[e] = power(ve);
+        a.s.k[e] = power2(ke);
+        a.s.v[e] = power2(ve);
     }
 }
 
@@ -330,9 +324,9 @@ MW4_DEV void write_rows(const Append8Args& a, const Side& side, const Rows& rw, 
             }
             top = __shfl_sync(0xffffffffu, top, rw.last);
         }
-        int e = scale_exponent(two_of<T>(top).x);
+        int e = scale_exponent(Pair16<T>::unpack(top).x);
         if (in_block) e = max(e, exponent_of(was));
-        const float now = power(e), inv = power(-e);
+        const float now = power2(e), inv = power2(-e);
         const bool leads = there && lane == rw.lead;
 #pragma unroll 1
         for (unsigned grown = __ballot_sync(0xffffffffu, leads && in_block && now != was); grown; grown &= grown - 1) {
@@ -453,14 +447,14 @@ __global__ void __launch_bounds__(kLongThreads, long_ctas(D)) kv8_append_long_ke
                 if (e < pieces) x[j] = *reinterpret_cast<const uint4*>(side.src + (run.row + e / P) * side.stride + e % P * 8);
             }
             const uint32_t bits = largest_finite<T>(x, (pieces + THREADS - 1) / THREADS);
-            float top = two_of<T>(__reduce_max_sync(0xffffffffu, bits)).x;
+            float top = Pair16<T>::unpack(__reduce_max_sync(0xffffffffu, bits)).x;
             if (lane == 0) sh_top[turn & 1][warp] = top;   // (two places in turn: nobody is two runs behind)
             team_sync(1 + team, THREADS);
 #pragma unroll
             for (int j = 0; j < TEAM; ++j) top = fmaxf(top, sh_top[turn & 1][team * TEAM + j]);
             int e = scale_exponent(top);
             if (in_block) e = max(e, exponent_of(before));
-            const float now = power(e), inv = power(-e);
+            const float now = power2(e), inv = power2(-e);
             uint8_t* to = side.pool + side.codes(a, run.page, run.in_page);
             if (in_block && now != before)                 // the block's other tokens follow
                 follow(to - in_block * a.c.slot_stride, a.c.slot_stride, block, D / 16, in_block, in_block + run.count - 1,
@@ -547,15 +541,8 @@ constexpr int kReadThreads = 256;
 
 template <typename T>
 MW4_DEV uint32_t value_pair(uint32_t two, float scale) {
-    const uint32_t h = f16x2_of_codes((uint16_t)two);
-    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
-    if constexpr (sizeof(T) == sizeof(__half) && std::is_same<T, __half>::value) {
-        const __half2 v = __floats2half2_rn(f.x * scale, f.y * scale);
-        return *reinterpret_cast<const uint32_t*>(&v);
-    } else {
-        const __nv_bfloat162 v = __floats2bfloat162_rn(f.x * scale, f.y * scale);
-        return *reinterpret_cast<const uint32_t*>(&v);
-    }
+    const float2 f = Pair16<__half>::unpack(f16x2_of_codes((uint16_t)two));
+    return Pair16<T>::pack(f.x * scale, f.y * scale);
 }
 template <typename T>
 MW4_DEV uint4 values8(const uint2& c, float scale) {

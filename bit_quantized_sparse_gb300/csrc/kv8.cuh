@@ -37,6 +37,8 @@ inline Scales scales_of(const moe_w4_kv8_cache& c) {
     return {c.k_scale, c.v_scale, c.scale_page_stride, c.scale_head_stride, shift};
 }
 
+// 2^e, -126 <= e <= 127.
+MW4_DEV float power2(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
 // Two codes to two fp16, exact.
 MW4_DEV uint32_t f16x2_of_codes(uint16_t c) {
     uint32_t r;

@@ -49,27 +49,11 @@ struct RopeArgs {
     float eps, offset, scale;
 };
 
-template <typename T> struct Pair16;
-template <> struct Pair16<__nv_bfloat16> {
-    MW4_DEV static float2 get(uint32_t u) { return __bfloat1622float2(*reinterpret_cast<__nv_bfloat162*>(&u)); }
-    MW4_DEV static uint32_t put(float a, float b) {
-        __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
-        return *reinterpret_cast<uint32_t*>(&v);
-    }
-};
-template <> struct Pair16<__half> {
-    MW4_DEV static float2 get(uint32_t u) { return __half22float2(*reinterpret_cast<__half2*>(&u)); }
-    MW4_DEV static uint32_t put(float a, float b) {
-        __half2 v = __floats2half2_rn(a, b);
-        return *reinterpret_cast<uint32_t*>(&v);
-    }
-};
-
 // Four values of a row: as packed pairs they multiply two at a time.
 struct Four {
     float2 x, y;
 };
-template <typename T> MW4_DEV Four four_of(const uint2& u) { return {Pair16<T>::get(u.x), Pair16<T>::get(u.y)}; }
+template <typename T> MW4_DEV Four four_of(const uint2& u) { return {Pair16<T>::unpack(u.x), Pair16<T>::unpack(u.y)}; }
 MW4_DEV Four mul(const Four& a, const Four& b) { return {__fmul2_rn(a.x, b.x), __fmul2_rn(a.y, b.y)}; }
 MW4_DEV Four mul_add(const Four& a, const Four& b, const Four& c) { return {__ffma2_rn(a.x, b.x, c.x), __ffma2_rn(a.y, b.y, c.y)}; }
 MW4_DEV Four all(float f) { return {make_float2(f, f), make_float2(f, f)}; }
@@ -167,8 +151,8 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas) qk_norm_rope_kernel(c
                 if (PAIRED) merge(u, v);
             }
             if (mine + i * a.step < a.n) {
-                *reinterpret_cast<uint2*>(y) = make_uint2(Pair16<T>::put(u.x.x, u.x.y), Pair16<T>::put(u.y.x, u.y.y));
-                *reinterpret_cast<uint2*>(y + (d2 - d1)) = make_uint2(Pair16<T>::put(v.x.x, v.x.y), Pair16<T>::put(v.y.x, v.y.y));
+                *reinterpret_cast<uint2*>(y) = make_uint2(Pair16<T>::pack(u.x.x, u.x.y), Pair16<T>::pack(u.y.x, u.y.y));
+                *reinterpret_cast<uint2*>(y + (d2 - d1)) = make_uint2(Pair16<T>::pack(v.x.x, v.x.y), Pair16<T>::pack(v.y.x, v.y.y));
             }
         }
         if (a.n - base <= ROWS * a.step) return;
