@@ -13,12 +13,14 @@
 // a warp has 32 tokens of a tile of 128, so that a unit of its ring is the same 32 D
 // bytes.  Rows that are short take attend_short.cu.
 //
-// Measured (kernels alone): 1 x 131,072 tokens, 2 kv heads of 256, group 8, codes: 28.7
+// Measured (kernels alone): 1 x 131,072 tokens, 2 kv heads of 256, group 8, codes: 29.2
 // us for 135 MB.  Its copies run at the copy rate for 19 us; 2 go before the first of
 // them (lengths, the list, page numbers), 2 to a row's end, 2 until the last CTA is
 // there, 3 to the join.  16 sequences of up to 32,768 tokens, 8 heads of 128, a scale
-// for each token: 38.6 for 189 MB; 8 x 40,000 with a window of 4096 14.7 for 34 MB; 16
-// bits, 32 of up to 8192 with a window of 1000, 8 heads of 128: 17.3 for 48 MB.
+// for each token: 38.9 for 189 MB; 8 x 40,000 with a window of 4096 15.0 for 34 MB; 16
+// bits, 32 of up to 8192 with a window of 1000, 8 heads of 128: 17.4 for 48 MB.  Groups of more
+// than 8 and heads of 64 wait for their own instructions, not for copies: 8 x 16,384, 4 of 128,
+// group 16: 43.9 for 135 MB; 4 x 116,918, 2 of 64, group 4: 37.6 for 120 MB.
 #include <climits>
 
 #include "attend_short.h"
@@ -28,8 +30,8 @@ namespace mw4 {
 
 // Ring units per warp and CTAs per SM for a head size; NB blocks of 8 query heads.
 // Over codes, two blocks of heads of 128 and three of 64: with 3 CTAs an SM registers would
-// spill, 96 and 300 bytes (8 x 16,384 tokens, 4 kv heads of 128, group 16: 54.2 us, with 2 40.2,
-// and with rings of 5 units 40.7; 16 x 8192, 4 of 64, group 24: 53.7, with 2 42.8).
+// spill, 54 and 62 bytes (8 x 16,384 tokens, 4 kv heads of 128, group 16: 47.5 us, with 2 43.9,
+// and with rings of 5 units 44.8; 16 x 8192, 4 of 64, group 24: 44.5, with 2 43.3).
 template <bool E8, int D, int NB> struct ListCfg;
 template <bool E8, int NB> struct ListCfg<E8, 64, NB> {
     static constexpr int slots = E8 && NB == 3 ? 8 : 5, ctas = NB == 1 ? 4 : E8 && NB == 3 ? 2 : 3;
@@ -336,7 +338,9 @@ static cudaError_t launch_list_win(const AttendArgs& a, const Scales& s, cudaStr
     return e;
 }
 
-// (16-bit values without a window have a kernel of their own)
+// (16-bit values without a window have a kernel of their own, which keeps a block's queries in registers and has
+// no arithmetic of windows: 1 x 131,072, 16/2 heads of 256: 45.4 us, through this one 46.5; 16 x 30,000, 24/8 of
+// 64: 152 and 172; 8 x 16,384, 96/4 of 128: 55.5 and 63.6)
 template <typename T, bool E8, int D, int NB>
 static cudaError_t launch_list(const AttendArgs& a, const Scales& s, cudaStream_t st) {
     if (!E8 || a.window) return launch_list_win<T, E8, D, NB, true>(a, s, st);

@@ -22,7 +22,7 @@ constexpr int kShortCtas = 8;      // CTAs of a row at most: a portable cluster,
 
 // CTAs of an SM that registers leave room for, for a head size and blocks of 8 query
 // heads; and ring units per warp: a CTA has a few tiles at most, and more units only
-// add turns before the first product (1 x 300: 6.7 us with 2, 7.3 with 4).
+// add turns before the first product (1 x 300: 7.2 us with 2, 7.6 with 4).
 constexpr int short_per_sm(int dim, int blocks) { return dim == 256 || (dim == 128 && blocks == 3) ? 2 : dim == 128 || blocks == 3 ? 3 : 4; }
 template <int D, int NB> struct ShortCfg {
     static constexpr int slots = NB == 3 ? 3 : 2, ctas = short_per_sm(D, NB);
@@ -230,11 +230,11 @@ static cudaError_t launch_short_dim(int dim, const AttendArgs& a, const Scales& 
 // lengths; clusters that fill the GPU keep up longer, those of 16-bit values twice as
 // many tiles, which have half the tokens and, being of a window, are alike in every row.
 // In us, list / clusters, rows of equal lengths, group 8.  Codes, heads of 256: 2 rows of
-// 1000 tokens, 1 tile a CTA, 9.2 / 7.8; 16 of 2000, 2, 10.8 / 11.8; 32 of 3000, 3 that fill
-// the GPU, 16.5 / 14.5; 256 of 1000, 8, 29.7 / 24.4, of 4000, 32, 84.5 / 81.0; heads of 128:
-// 16 of 2000, 2, 10.2 / 9.7; 256 of 500, 4, 15.6 / 12.8, of 2000, 16, 29.9 / 34.5; of 64: 8 of
-// 3000, 3, 9.2 / 8.8; 512 of 1000, 8, 25.2 / 20.0.  16 bits: heads of 64, 512 of 1000, 16,
-// 34.5 / 26.3; of 128, 256 of 500, 8, 18.3 / 15.5; of 256, 256 of 1000, 16, 46.7 / 42.7.
+// 1000 tokens, 1 tile a CTA, 9.3 / 8.1; 16 of 2000, 2, 11.1 / 12.3; 32 of 3000, 3 that fill
+// the GPU, 17.1 / 15.5; 256 of 1000, 8, 31.8 / 26.2, of 4000, 32, 84.2 / 83.4; heads of 128:
+// 16 of 2000, 2, 10.3 / 9.9; 256 of 500, 4, 16.3 / 13.7, of 2000, 16, 31.4 / 37.6; of 64: 8 of
+// 3000, 3, 9.2 / 9.0; 512 of 1000, 8, 26.7 / 21.5.  16 bits: heads of 64, 512 of 1000, 16,
+// 34.4 / 26.4; of 128, 256 of 500, 8, 18.8 / 15.7; of 256, 256 of 1000, 16, 46.8 / 41.8.
 int short_ctas(const AttendArgs& a, int dim, bool e8) {
     const int64_t rows = (int64_t)a.c.n_seqs * a.c.n_kv_heads * a.head_blocks;
     if ((int64_t)a.c.n_kv_heads * a.head_blocks > 65535) return 0;   // of a grid's dimension

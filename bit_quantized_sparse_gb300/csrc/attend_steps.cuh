@@ -10,7 +10,7 @@
 // multiplication a token, not the codes.  Queries are brought to fp16 by a power of
 // two per head, so that bf16 ones lose nothing.  (mma.sync takes E4M3 as well, and
 // queries can be sums of such terms, but it costs as much as the conversions and two
-// fp16 products: 1 x 131,072 tokens 36.8 us so.)
+// fp16 products: 1 x 131,072 tokens 36.8 us so, where it was 29.9.)
 #pragma once
 #include "attend.cuh"
 #include "kv8.cuh"

@@ -249,6 +249,10 @@ class PagedKVCache8(PagedKVCache):
 
     kv_append chooses the scales: powers of two, which lose no bits of a code.  Weights and positions are not kept, and
     kv_evict does not take it: tokens of one block share a scale and cannot move one by one.
+
+    kv_append and kv_read take bfloat16 of any size.  attend_decode adds up in fp32: the values that it sees have to lie
+    below 2^80 in magnitude, and so has the scale of the scores times a head's largest query times a key's scale; scales
+    of the caller's own are finite and not negative.
     """
 
     def __init__(self, k, v, k_scale, v_scale, block_table, seq_lens, dtype=torch.bfloat16):
