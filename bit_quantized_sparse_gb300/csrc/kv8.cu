@@ -87,8 +87,8 @@ MW4_DEV void row_at(const Append8Args& a, int i, int& b, int& t) {
 }
 
 // Debug builds: a block whose tokens are not consecutive rows would be several runs', each with its
-// own scale.  Whether there is one costs a look at all rows from each, so the product does not ask; here
-// such a call writes nothing.
+// own scale.  Whether there is one takes a look at all rows (by CTAs beside the writing ones, 4096 tokens
+// 4.5 -> 11.3 us), so the product does not ask; here such a call writes nothing.
 MW4_DEV bool refused(const Append8Args& a) {
 #ifdef MW4_DEBUG_CHECKS
     return *a.disorder;
